@@ -22,10 +22,11 @@
  *   - No C++ exception crosses the ABI.  A non-OK status leaves a one-line
  *     explanation that ring_attn_last_error() returns (per host thread).
  *   - The library holds no device allocation of its own except static
- *     device variables of the module: three status words per device (bf16
- *     forward, backward and FP8 forward kernels), the fixed 4 MiB array of
- *     ring_attn_bwd_noalloc, and 64 work-queue counters.  Each kernel launch
- *     (one per forward call, two per backward call) takes the next counter
+ *     device variables of the module: a status word per device for each
+ *     group of kernels (bf16 forward, backward, FP8 forward, 4-bit cache,
+ *     cache attention), the fixed 4 MiB array of ring_attn_bwd_noalloc, and
+ *     64 work-queue counters.  Each launch of a forward or
+ *     backward kernel (one per forward call, two per backward call) takes the next counter
  *     in rotation and zeroes it with a memset ordered on `stream`, so up to
  *     64 launches may be in flight on different streams at once, and CUDA
  *     graph replays start from zero.
@@ -338,14 +339,158 @@ ra_status ring_attn_fwd_fp8(const void* q8, const void* k8, const void* v8, cons
                             int Hkv, int64_t L, int d, int n_ring, int causal, float scale,
                             ra_stream_t stream);
 
+/* Element types of the cache entry points below. */
+enum { RA_BF16 = 0, RA_FP16 = 1, RA_FP32 = 2 };
+
+/*
+ * The paged 4-bit K/V cache.  Once a sequence has gone through the forward
+ * pass its keys and values are kept in 4 bits for the tokens that follow:
+ * ring_attn_kv4_plan gives the requests of a batch their pages,
+ * ring_attn_kv4_append quantises new keys and values into them,
+ * ring_attn_kv4_fwd attends over them, ring_attn_kv4_read takes values out.
+ *
+ *   cache   uint8 [num_pages, Hkv, page / 16, 16 (d + 8)], contiguous,
+ *           16-byte aligned; page (tokens a page) a multiple of 16 up to
+ *           4096, d 64 or 128, num_pages * page < 2^31.  The last axis is one
+ *           block, 16 tokens of one page and head: K codes (16 rows of d / 2
+ *           bytes, element 2i in the low nibble of byte i), 16 (step, zero)
+ *           fp16 pairs of K, V codes, 16 pairs of V.  The V codes of the
+ *           keys 8h + 2t + s (h, s < 2, t < 4) and the elements
+ *           g d/8 + 4w + 2b + n (g < 8, w < d/32, b, n < 2) are in byte
+ *           [h][g][t][w][s][b], n = 0 in the low nibble.
+ *   value   step * code + zero.  Of a vector x of one token and head, clamped
+ *           to +-65504: zero = fp16(min x), step = (max x - min x) / 15 in
+ *           fp32, rounded to fp16 towards zero, at least 2^-24; code = the
+ *           nearest of 0..15 to (x - zero) / step, ties to even.  A vector
+ *           that holds a NaN reads as NaN.
+ *   slot    page index * page + place in the page, of one token; -1: none.
+ *
+ * Indices in device memory cannot be checked by the host.  The kernels check
+ * them where they use them: a slot, page index, length or row start outside
+ * its tensor is left out (length and starts: cut down to the tensor) and
+ * reported by ring_attn_check_status as RA_ERR_INVALID_ARG.
+ */
+
+/*
+ * ring_attn_kv4_plan -- block tables and slot maps of one step of a batch.
+ *
+ * add[r] >= 0 gives request r that many new tokens, -1 ends it.  In one call:
+ * the pages of the ended requests go back on the stack of free pages, in the
+ * order of the requests and of their tables; then every other request gets
+ * the pages it needs, ceil((len + add) / page) - ceil(len / page) of them, in
+ * the order of the requests, each from the top of the stack; then each new
+ * token gets its slot.
+ *
+ *   lens, add   int32 [R]               tokens held; tokens to add          (in)
+ *   table       int32 [R, W]            page indices                         (in)
+ *   pool        int32 [num_pages + 1]   pool[0] free pages, pool[1..] the
+ *                                       stack, its top last                  (in)
+ *   lens_out, table_out, pool_out       the same after the step: 0 tokens and
+ *                                       -1 entries for an ended request, -1
+ *                                       above the top of the stack          (out)
+ *   cu          int32 [R + 1]           new tokens before each request      (out)
+ *   slots       int32 [max_tokens]      the new tokens' slots, -1 behind
+ *                                       the last one                        (out)
+ *   shortage    int32 [1]               0, or: the pages that are missing;
+ *                                       -1 for numbers that do not fit (a
+ *                                       length below 0 or above W * page, an
+ *                                       add below -1, more than max_tokens
+ *                                       tokens, a stack beyond num_pages)   (out)
+ * With a shortage nothing changes: the outputs are the inputs, cu is 0 and
+ * every slot -1.  Entries of the table beyond a request's pages are not read.
+ *
+ * Each of lens_out, table_out, pool_out is either the input itself or does not
+ * overlap any other argument.  R <= 8192, W >= 1, R * W < 2^31,
+ * W * page <= 2^30, 0 <= max_tokens < 2^31, page in [1, 4096].  Pointers
+ * 4-byte aligned.  One launch.
+ */
+ra_status ring_attn_kv4_plan(const int32_t* lens, const int32_t* add, const int32_t* table,
+                             const int32_t* pool, int32_t* lens_out, int32_t* table_out,
+                             int32_t* pool_out, int32_t* cu, int32_t* slots, int32_t* shortage,
+                             int R, int W, int num_pages, int page, int64_t max_tokens,
+                             ra_stream_t stream);
+
+/*
+ * ring_attn_kv4_append -- quantise k and v of T tokens into their slots.
+ *
+ *   k, v    bf16 or fp16 (`dtype`) [T, Hkv, d]; a token's [Hkv, d] is
+ *           contiguous, tokens are k_stride (v_stride) elements apart, a
+ *           multiple of 8 and at least Hkv * d; 16-byte aligned         (in)
+ *   slots   int32 [T]; a token with slot -1 is not written.  The slots
+ *           of a call are distinct.                                     (in)
+ *   cache                                                           (in/out)
+ */
+ra_status ring_attn_kv4_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                               const int32_t* slots, void* cache, int64_t T, int Hkv, int d,
+                               int dtype, int num_pages, int page, ra_stream_t stream);
+
+/*
+ * ring_attn_kv4_read -- the cached values of T slots.
+ *
+ *   slots   int32 [T], in any order, the same one as often as wanted   (in)
+ *   k, v    `dtype` (RA_BF16, RA_FP16, RA_FP32) [T, Hkv, d], rounded to
+ *           nearest even from fp32; zeros for slot -1; 16-byte aligned (out)
+ */
+ra_status ring_attn_kv4_read(const void* cache, const int32_t* slots, void* k, void* v, int64_t T,
+                             int Hkv, int d, int dtype, int num_pages, int page,
+                             ra_stream_t stream);
+
+/*
+ * ring_attn_kv4_workspace_size -- bytes of device workspace that any call of
+ * ring_attn_kv4_fwd needs.  The workspace is zeroed once, before its first
+ * call; each call leaves it ready for the next one.  Calls that may run at the same
+ * time (streams, replays of captured graphs) need one each.  After
+ * RA_ERR_TIMEOUT it has to be zeroed again.
+ */
+ra_status ring_attn_kv4_workspace_size(size_t* bytes);
+
+/*
+ * ring_attn_kv4_fwd -- attention of new query tokens over cached ones.
+ *
+ * For query token t < n of request r (rows cu[r] .. cu[r + 1] of q, n of them;
+ * with cu NULL, T must be R and request r has the one row r) and query head
+ * h, over the cached tokens c < lens[r], when causal c < lens[r] - n + t + 1
+ * (the query tokens are the last ones cached):
+ *     out = sum_c softmax_c(scale * q . k[c, h / g]) v[c, h / g]
+ *     lse = ln sum_c exp(scale * q . k[c, h / g])
+ * g = Hq / Hkv.  A row that sees no token gets out = 0, lse = -inf.  Rows from
+ * cu[R] on are left as they are.  The results of caches that hold different parts of a
+ * sequence (causal = 0 for the earlier ones) merge with ring_attn_merge,
+ * which takes out as RA_FP32 and lse in this layout.
+ *
+ *   q        bf16 or fp16 (`dtype`) [T, Hq, d]; a token's [Hq, d] is
+ *            contiguous, tokens are q_stride elements apart, a multiple of 8
+ *            and at least Hq * d                                       (in)
+ *   cache    num_pages, Hkv, page, d as above                          (in)
+ *   table    int32 [R, W]: page table[r, c / page] holds token c       (in)
+ *   lens     int32 [R], 0 allowed                                      (in)
+ *   cu       int32 [R + 1] or NULL                                     (in)
+ *   out      [T, Hq, d] of q's type, or fp32 (`out_dtype`)            (out)
+ *   lse      fp32 [T, Hq], natural log                                (out)
+ *   max_q    at least the most query tokens of a request; chooses the kernel,
+ *            the result does not need it to be tight
+ *   workspace  ring_attn_kv4_workspace_size bytes                  (in/out)
+ *
+ * T < 2^31, Hq % Hkv == 0, W >= 1, W * page <= 2^30.  Pointers 16-byte
+ * aligned (table, lens, cu, lse: 4).  out and lse must not overlap the inputs
+ * or each other.  T == 0 or R == 0 launches nothing.
+ */
+ra_status ring_attn_kv4_fwd(const void* q, int64_t q_stride, const void* cache,
+                            const int32_t* table, const int32_t* lens, const int32_t* cu,
+                            void* out, float* lse, int64_t T, int R, int Hq, int Hkv, int d, int W,
+                            int num_pages, int page, int max_q, int causal, float scale, int dtype,
+                            int out_dtype, void* workspace, size_t workspace_bytes,
+                            ra_stream_t stream);
+
 /*
  * ring_attn_check_status -- synchronise `stream`, then read and clear the
  * device status words of the current device.  Every device-side wait of the
  * forward (bf16 and FP8) and backward kernels is bounded (see
  * ring_attn_set_wait_limit_ns); a wait that
  * runs out makes the kernel record RA_ERR_TIMEOUT, release its tensor memory
- * and return, leaving the CUDA context usable.  Returns RA_ERR_CUDA if the
- * synchronisation itself fails.
+ * and return, leaving the CUDA context usable.  The 4-bit cache kernels
+ * record RA_ERR_INVALID_ARG for an index on the device that is out of range.
+ * Returns RA_ERR_CUDA if the synchronisation itself fails.
  */
 ra_status ring_attn_check_status(ra_stream_t stream);
 

@@ -37,6 +37,12 @@ SIGNATURES = {
     "ring_attn_fwd_fp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I64, _I, _I, _I,
                                ctypes.c_float, _P]),
     "ring_attn_merge": (_I, [_P, _P, _P, _P, _P, _P, _I64, _I, _P]),
+    "ring_attn_kv4_plan": (_I, [_P] * 10 + [_I, _I, _I, _I, _I64, _P]),
+    "ring_attn_kv4_append": (_I, [_P, _I64, _P, _I64, _P, _P, _I64, _I, _I, _I, _I, _I, _P]),
+    "ring_attn_kv4_read": (_I, [_P, _P, _P, _P, _I64, _I, _I, _I, _I, _I, _P]),
+    "ring_attn_kv4_workspace_size": (_I, [ctypes.POINTER(ctypes.c_size_t)]),
+    "ring_attn_kv4_fwd": (_I, [_P, _I64, _P, _P, _P, _P, _P, _P, _I64] + [_I] * 9 +
+                          [ctypes.c_float, _I, _I, _P, ctypes.c_size_t, _P]),
     "ring_attn_check_status": (_I, [_P]),
     "ring_attn_set_wait_limit_ns": (_I, [ctypes.c_uint64]),
     "ring_attn_set_max_ctas": (_I, [_I]),
@@ -143,6 +149,42 @@ def ring_attn_fwd_fp8(q8, k8, v8, sq, sk, sv, out, lse, B, Hq, Hkv, L, d, n_ring
 
 def ring_attn_merge(o_a, lse_a, o_b, lse_b, o_out, lse_out, rows, d, stream=0):
     return _check(load().ring_attn_merge(o_a, lse_a, o_b, lse_b, o_out, lse_out, rows, d, stream))
+
+
+RA_BF16, RA_FP16, RA_FP32 = 0, 1, 2
+
+
+def ring_attn_kv4_plan(lens, add, table, pool, lens_out, table_out, pool_out, cu, slots, shortage,
+                       R, W, num_pages, page, max_tokens, stream=0):
+    return _check(load().ring_attn_kv4_plan(lens, add, table, pool, lens_out, table_out, pool_out,
+                                            cu, slots, shortage, R, W, num_pages, page,
+                                            max_tokens, stream))
+
+
+def ring_attn_kv4_append(k, k_stride, v, v_stride, slots, cache, T, Hkv, d, dtype, num_pages, page,
+                         stream=0):
+    return _check(load().ring_attn_kv4_append(k, k_stride, v, v_stride, slots, cache, T, Hkv, d,
+                                              dtype, num_pages, page, stream))
+
+
+def ring_attn_kv4_read(cache, slots, k, v, T, Hkv, d, dtype, num_pages, page, stream=0):
+    return _check(load().ring_attn_kv4_read(cache, slots, k, v, T, Hkv, d, dtype, num_pages, page,
+                                            stream))
+
+
+def ring_attn_kv4_workspace_size() -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().ring_attn_kv4_workspace_size(ctypes.byref(n)))
+    return n.value
+
+
+def ring_attn_kv4_fwd(q, q_stride, cache, table, lens, cu, out, lse, T, R, Hq, Hkv, d, W,
+                      num_pages, page, max_q, causal, scale, dtype, out_dtype, workspace,
+                      workspace_bytes, stream=0):
+    return _check(load().ring_attn_kv4_fwd(q, q_stride, cache, table, lens, cu, out, lse, T, R, Hq,
+                                           Hkv, d, W, num_pages, page, max_q, int(bool(causal)),
+                                           scale, dtype, out_dtype, workspace, workspace_bytes,
+                                           stream))
 
 
 def ring_attn_check_status(stream=0):

@@ -305,6 +305,241 @@ def merge(o_a: torch.Tensor, lse_a: torch.Tensor, o_b: torch.Tensor, lse_b: torc
     return out, lse_out
 
 
+# ---------------------------------------------------------------- 4-bit K/V cache
+_CODE = {torch.bfloat16: _lib.RA_BF16, torch.float16: _lib.RA_FP16, torch.float32: _lib.RA_FP32}
+_workspace_bytes = None
+
+
+class _Here:
+    """``_on`` where nothing has to be switched: the tensors' device is the
+    current one and the call uses its current stream."""
+
+    __slots__ = ("handle",)
+
+    def __init__(self, handle):
+        self.handle = handle
+
+    def __enter__(self):
+        return self.handle
+
+    def __exit__(self, *exc):
+        return False
+
+
+def _here(device, stream):
+    if stream is None and torch.cuda.current_device() == device.index:
+        return _Here(torch.cuda.current_stream(device).cuda_stream)
+    return _on(device, stream)
+
+
+def _check_same_device(device, **tensors):
+    for n, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{n} is on {t.device}, expected {device}")
+
+
+def _check_rows(t: torch.Tensor, name: str):
+    """[T, H, d] whose tokens may be strided (a slice of a fused projection),
+    each token's [H, d] contiguous.  Returns the token stride in elements."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16 and t.dtype != torch.float16:
+        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be a 3-d tensor [T, H, d]")
+    T, H, d = t.shape
+    st = t.stride()
+    if T == 0 or t.is_contiguous():
+        return H * d
+    if (d > 1 and st[2] != 1) or (H > 1 and st[1] != d):
+        raise ValueError(f"each token's [H, d] of {name} must be contiguous")
+    if T == 1:
+        return H * d
+    if st[0] < H * d:
+        raise ValueError(f"the tokens of {name} must not overlap (stride {st[0]})")
+    return st[0]
+
+
+def _cache_shape(cache: torch.Tensor):
+    """(num_pages, Hkv, page, d) of a cache tensor."""
+    _check_cuda(cache, "cache", torch.uint8, 4)
+    P, Hkv, blocks, nbytes = cache.shape
+    d = nbytes // 16 - 8
+    if nbytes != 16 * (d + 8) or d not in (64, 128) or blocks < 1 or Hkv < 1:
+        raise ValueError(f"cache must be [num_pages, Hkv, page / 16, 16 * (d + 8)] with d 64 or "
+                         f"128, got {tuple(cache.shape)}")
+    return P, Hkv, 16 * blocks, d
+
+
+def kv4_cache(num_pages: int, Hkv: int, d: int, page: int = 64, device="cuda") -> torch.Tensor:
+    """An empty paged 4-bit K/V cache: uint8 [num_pages, Hkv, page / 16,
+    16 * (d + 8)], d 64 or 128, page a multiple of 16."""
+    if d not in (64, 128):
+        raise ValueError(f"d must be 64 or 128, got {d}")
+    if page < 16 or page > 4096 or page % 16 != 0:
+        raise ValueError(f"page must be a multiple of 16 up to 4096, got {page}")
+    if num_pages < 0 or Hkv < 1:
+        raise ValueError("num_pages must be >= 0 and Hkv >= 1")
+    return torch.zeros((num_pages, Hkv, page // 16, 16 * (d + 8)), dtype=torch.uint8, device=device)
+
+
+def kv4_pool(num_pages: int, device="cuda") -> torch.Tensor:
+    """The stack of free pages of a new cache, int32 [num_pages + 1]: its
+    size, then the pages, of which 0 is taken first."""
+    return torch.arange(num_pages, -1, -1, dtype=torch.int32, device=device)
+
+
+def kv4_plan(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, pool: torch.Tensor,
+             page: int, max_tokens: int, out=None, stream=None):
+    """Block tables and slot maps of one step of a batch, on the GPU.
+    lens [R]: cached tokens of each request; add [R]: new ones, -1 ends the
+    request; table [R, W]: its pages; pool [num_pages + 1]: the stack of free
+    pages (``kv4_pool``); all int32.  Ended requests give their pages back,
+    then the others take what they need in their order.
+
+    Returns (lens, table, pool, cu [R + 1], slots [max_tokens], shortage [1]):
+    the state after the step, the new tokens before each request, their slots
+    (-1 behind the last) and 0, or how many pages are missing (-1: numbers
+    that do not fit), in which case nothing changes.  ``out``: tensors of
+    these shapes for the results; the first three may be the inputs
+    themselves."""
+    for t, n, k in ((lens, "lens", 1), (add, "add", 1), (table, "table", 2), (pool, "pool", 1)):
+        _check_cuda(t, n, torch.int32, k)
+    R, W = table.shape
+    if lens.shape[0] != R or add.shape[0] != R:
+        raise ValueError(f"lens {tuple(lens.shape)}, add {tuple(add.shape)} and table "
+                         f"{tuple(table.shape)} do not belong together")
+    num_pages = pool.shape[0] - 1
+    if num_pages < 0:
+        raise ValueError("pool must be [num_pages + 1]")
+    dev = table.device
+    _check_same_device(dev, lens=lens, add=add, pool=pool)
+    with _here(dev, stream) as sh:
+        if out is None:
+            out = (torch.empty_like(lens), torch.empty_like(table), torch.empty_like(pool),
+                   torch.empty(R + 1, dtype=torch.int32, device=dev),
+                   torch.empty(max_tokens, dtype=torch.int32, device=dev),
+                   torch.empty(1, dtype=torch.int32, device=dev))
+        else:
+            for t, n, shape in zip(out, ("lens", "table", "pool", "cu", "slots", "shortage"),
+                                   ((R,), (R, W), (num_pages + 1,), (R + 1,), (max_tokens,), (1,)),
+                                   strict=True):
+                _check_out(t, "out " + n, torch.int32, shape)
+                _check_same_device(dev, **{"out_" + n: t})
+        lo, to, po, cu, slots, shortage = out
+        _lib.ring_attn_kv4_plan(lens.data_ptr(), add.data_ptr(), table.data_ptr(), pool.data_ptr(),
+                                lo.data_ptr(), to.data_ptr(), po.data_ptr(), cu.data_ptr(),
+                                slots.data_ptr(), shortage.data_ptr(), R, W, num_pages, page,
+                                max_tokens, sh)
+    return lo, to, po, cu, slots, shortage
+
+
+def kv4_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,
+               stream=None):
+    """Quantise k, v [T, Hkv, d] (bf16 or fp16; tokens may be strided) into
+    the cache at ``slots`` (int32 [T], distinct; -1 skips a token)."""
+    ks, vs = _check_rows(k, "k"), _check_rows(v, "v")
+    P, Hkv, page, d = _cache_shape(cache)
+    T = k.shape[0]
+    if k.shape != (T, Hkv, d) or v.shape != k.shape or k.dtype != v.dtype:
+        raise ValueError(f"k {tuple(k.shape)} {k.dtype} and v {tuple(v.shape)} {v.dtype} must be "
+                         f"[T, {Hkv}, {d}] of one type")
+    _check_out(slots, "slots", torch.int32, (T,))
+    _check_same_device(cache.device, k=k, v=v, slots=slots)
+    with _here(cache.device, stream) as sh:
+        _lib.ring_attn_kv4_append(k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(),
+                                  cache.data_ptr(), T, Hkv, d, _CODE[k.dtype], P, page, sh)
+    return cache
+
+
+def kv4_read(cache: torch.Tensor, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+             k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
+    """The cached keys and values at ``slots`` (int32 [T]; zeros for -1):
+    (k, v) of ``dtype`` (bf16, fp16 or fp32), [T, Hkv, d]."""
+    P, Hkv, page, d = _cache_shape(cache)
+    _check_cuda(slots, "slots", torch.int32, 1)
+    if dtype not in _CODE:
+        raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
+    T = slots.shape[0]
+    dev = cache.device
+    _check_same_device(dev, slots=slots, k=k, v=v)
+    with _here(dev, stream) as sh:
+        k = torch.empty((T, Hkv, d), dtype=dtype, device=dev) if k is None else k
+        v = torch.empty((T, Hkv, d), dtype=dtype, device=dev) if v is None else v
+        _check_out(k, "k", dtype, (T, Hkv, d))
+        _check_out(v, "v", dtype, (T, Hkv, d))
+        _lib.ring_attn_kv4_read(cache.data_ptr(), slots.data_ptr(), k.data_ptr(), v.data_ptr(), T,
+                                Hkv, d, _CODE[dtype], P, page, sh)
+    return k, v
+
+
+def kv4_workspace(device="cuda") -> torch.Tensor:
+    """A workspace for ``kv4_fwd``, zeroed as it has to be.  One serves any
+    number of calls that run one after the other."""
+    global _workspace_bytes
+    if _workspace_bytes is None:
+        _workspace_bytes = _lib.ring_attn_kv4_workspace_size()
+    return torch.zeros(_workspace_bytes, dtype=torch.uint8, device=device)
+
+
+def kv4_fwd(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+            cu: torch.Tensor | None = None, causal: bool = True, scale: float | None = None,
+            max_q: int | None = None, out: torch.Tensor | None = None,
+            lse: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+            workspace: torch.Tensor | None = None, stream=None):
+    """Attention of new query tokens over the cached tokens of R requests.
+    q [T, Hq, d] (bf16 or fp16; tokens may be strided); table int32 [R, W],
+    lens int32 [R] and cu int32 [R + 1] as ``kv4_plan`` gives them: request
+    r's query tokens are the rows cu[r] .. cu[r + 1] (without cu: one a
+    request), its keys the first lens[r] cached tokens; causal: the query
+    tokens are the last of these.  Returns (out [T, Hq, d] of q's type or
+    ``out_dtype`` float32, lse fp32 [T, Hq]); rows from cu[R] on are not
+    written.  ``max_q`` bounds the query tokens of a request (default T).
+    ``workspace`` (``kv4_workspace``) is allocated and zeroed if omitted."""
+    qs = _check_rows(q, "q")
+    P, Hkv, page, d = _cache_shape(cache)
+    T, Hq, dq = q.shape
+    if dq != d or Hq % Hkv != 0 or Hq < 1:
+        raise ValueError(f"q {tuple(q.shape)} does not match a cache of {Hkv} heads of {d}")
+    _check_cuda(table, "table", torch.int32, 2)
+    R, W = table.shape
+    _check_out(lens, "lens", torch.int32, (R,))
+    if cu is not None:
+        _check_out(cu, "cu", torch.int32, (R + 1,))
+    elif T != R:
+        raise ValueError(f"without cu every request has one query token, got {T} for {R} requests")
+    if max_q is None:
+        max_q = T
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    dev = q.device
+    _check_same_device(dev, cache=cache, table=table, lens=lens, cu=cu, out=out, lse=lse,
+                       workspace=workspace)
+    if out_dtype is None:
+        out_dtype = q.dtype if out is None else out.dtype
+    if out_dtype != q.dtype and out_dtype != torch.float32:
+        raise TypeError(f"the output is {q.dtype} or float32, got {out_dtype}")
+    with _here(dev, stream) as sh:
+        if out is None:
+            out = torch.empty((T, Hq, d), dtype=out_dtype, device=dev)
+        else:
+            _check_out(out, "out", out_dtype, (T, Hq, d))
+        if lse is None:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        else:
+            _check_out(lse, "lse", torch.float32, (T, Hq))
+        if workspace is None:
+            workspace = kv4_workspace(dev)
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        _lib.ring_attn_kv4_fwd(q.data_ptr(), qs, cache.data_ptr(), table.data_ptr(),
+                               lens.data_ptr(), 0 if cu is None else cu.data_ptr(), out.data_ptr(),
+                               lse.data_ptr(), T, R, Hq, Hkv, d, W, P, page, max_q, causal, scale,
+                               _CODE[q.dtype], _CODE[out_dtype], workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), sh)
+    return out, lse
+
+
 def check_status(stream=None):
     with torch.cuda.device(torch.cuda.current_device()):
         _lib.ring_attn_check_status(_stream_handle(stream))

@@ -111,6 +111,21 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_if(uint32_t bar, uint32_t 
       :: "r"(bar), "r"(bytes), "r"(issue) : "memory");
 }
 
+// Untiled bulk copy global -> shared (both 16-byte aligned, a multiple of 16
+// bytes), completion counted in bytes on an mbarrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar) : "memory");
+}
+
+// Order this thread's earlier generic accesses to shared memory before later
+// accesses to it by the async proxy (bulk copies, tcgen05 operands).
+__device__ __forceinline__ void fence_proxy_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" :: "l"(reinterpret_cast<uint64_t>(p)));
 }

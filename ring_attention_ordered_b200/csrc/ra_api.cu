@@ -276,6 +276,31 @@ ra_status check_forward_shape(int B, int Hq, int Hkv, int64_t L, int d, int n_ri
   return RA_OK;
 }
 
+// Shape of a 4-bit cache, shared by its entry points.
+ra_status check_kv4_cache(int Hkv, int d, int num_pages, int page) {
+  if (Hkv < 1) return fail(RA_ERR_INVALID_ARG, "Hkv must be >= 1 (got %d)", Hkv);
+  if (d != 64 && d != 128) return fail(RA_ERR_UNSUPPORTED, "head dim %d (supported: 64, 128)", d);
+  if (num_pages < 0) return fail(RA_ERR_INVALID_ARG, "num_pages must be >= 0 (got %d)", num_pages);
+  if (page < 16 || page > 4096 || page % 16 != 0)
+    return fail(RA_ERR_INVALID_ARG, "page must be a multiple of 16 up to 4096 (got %d)", page);
+  if (static_cast<long long>(num_pages) * page >= (1ll << 31))
+    return fail(RA_ERR_INVALID_ARG, "num_pages * page must be < 2^31");
+  if (static_cast<double>(num_pages) * Hkv * (page / 16) >= 2147483648.0)
+    return fail(RA_ERR_INVALID_ARG, "num_pages * Hkv * page / 16 must be < 2^31");
+  return RA_OK;
+}
+
+size_t kv4_cache_bytes(int Hkv, int d, int num_pages, int page) {
+  return static_cast<size_t>(num_pages) * Hkv * page * (d + 8);
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Bytes that T tokens of `width` contiguous elements, `stride` apart, span.
+size_t span_bytes(int64_t T, int64_t width, int64_t stride, int elem) {
+  return T == 0 ? 0 : (static_cast<size_t>(T - 1) * stride + width) * elem;
+}
+
 }  // namespace
 
 extern "C" {
@@ -663,6 +688,219 @@ ra_status ring_attn_fwd_fp8(const void* q8, const void* k8, const void* v8, cons
   return ok();
 }
 
+ra_status ring_attn_kv4_plan(const int32_t* lens, const int32_t* add, const int32_t* table,
+                             const int32_t* pool, int32_t* lens_out, int32_t* table_out,
+                             int32_t* pool_out, int32_t* cu, int32_t* slots, int32_t* shortage,
+                             int R, int W, int num_pages, int page, int64_t max_tokens,
+                             ra_stream_t stream) {
+  if (R < 0 || num_pages < 0 || max_tokens < 0)
+    return fail(RA_ERR_INVALID_ARG, "negative size (R=%d num_pages=%d max_tokens=%lld)", R,
+                num_pages, static_cast<long long>(max_tokens));
+  if (R > 8192) return fail(RA_ERR_UNSUPPORTED, "R=%d (supported: up to 8192 requests)", R);
+  if (W < 1 || static_cast<long long>(R) * W >= (1ll << 31))
+    return fail(RA_ERR_INVALID_ARG, "W must be >= 1 and R * W < 2^31 (R=%d W=%d)", R, W);
+  if (page < 1 || page > 4096)
+    return fail(RA_ERR_INVALID_ARG, "page must be in [1, 4096] (got %d)", page);
+  if (static_cast<long long>(W) * page > (1ll << 30))
+    return fail(RA_ERR_INVALID_ARG, "W * page must be <= 2^30");
+  if (max_tokens >= (1ll << 31)) return fail(RA_ERR_INVALID_ARG, "max_tokens must be < 2^31");
+  if (num_pages == 2147483647 || static_cast<long long>(num_pages) * page >= (1ll << 31))
+    return fail(RA_ERR_INVALID_ARG, "num_pages * page must be < 2^31");
+  const void* ptrs[10] = {lens, add, table, pool, lens_out, table_out, pool_out, cu, slots, shortage};
+  const size_t nR = static_cast<size_t>(R) * 4, nT = nR * W;
+  const size_t nP = (static_cast<size_t>(num_pages) + 1) * 4;
+  const size_t n[10] = {nR, nR, nT, nP, nR, nT, nP, nR + 4, static_cast<size_t>(max_tokens) * 4, 4};
+  for (int i = 0; i < 10; ++i) {
+    if (!ptrs[i] && n[i] != 0) return fail(RA_ERR_INVALID_ARG, "null pointer");
+    if (!aligned4(ptrs[i])) return fail(RA_ERR_INVALID_ARG, "pointers must be 4-byte aligned");
+  }
+  for (int o = 4; o < 10; ++o)
+    for (int i = 0; i < o; ++i) {
+      const bool in_place = (o == 4 && i == 0) || (o == 5 && i == 2) || (o == 6 && i == 3);
+      if (in_place && ptrs[o] == ptrs[i]) continue;
+      if (n[o] != 0 && n[i] != 0 && overlaps(ptrs[o], n[o], ptrs[i], n[i]))
+        return fail(RA_ERR_INVALID_ARG, "an output overlaps another argument");
+    }
+  int sms = 0;
+  ra_status st = device_info(&sms);
+  if (st != RA_OK) return st;
+  ra::Kv4PlanParams prm = {lens, add, table, pool, lens_out, table_out, pool_out, cu, slots,
+                           shortage, R, W, num_pages, page, max_tokens};
+  cudaError_t e = ra::launch_kv4_plan(prm, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(RA_ERR_CUDA, "plan launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+ra_status ring_attn_kv4_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                               const int32_t* slots, void* cache, int64_t T, int Hkv, int d,
+                               int dtype, int num_pages, int page, ra_stream_t stream) {
+  ra_status st = check_kv4_cache(Hkv, d, num_pages, page);
+  if (st != RA_OK) return st;
+  if (T < 0 || T >= (1ll << 31)) return fail(RA_ERR_INVALID_ARG, "T must be in [0, 2^31)");
+  if (dtype != RA_BF16 && dtype != RA_FP16)
+    return fail(RA_ERR_UNSUPPORTED, "dtype %d (supported: RA_BF16, RA_FP16)", dtype);
+  const int64_t width = static_cast<int64_t>(Hkv) * d;
+  if (k_stride < width || v_stride < width || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return fail(RA_ERR_INVALID_ARG, "token strides must be multiples of 8 and >= Hkv * d");
+  if (T == 0) return ok();
+  if (!k || !v || !slots || !cache) return fail(RA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(k) || !aligned16(v) || !aligned16(cache) || !aligned4(slots))
+    return fail(RA_ERR_INVALID_ARG, "k, v and cache must be 16-byte aligned, slots 4-byte aligned");
+  const size_t nc = kv4_cache_bytes(Hkv, d, num_pages, page);
+  if (nc != 0 && (overlaps(cache, nc, k, span_bytes(T, width, k_stride, 2)) ||
+                  overlaps(cache, nc, v, span_bytes(T, width, v_stride, 2)) ||
+                  overlaps(cache, nc, slots, static_cast<size_t>(T) * 4)))
+    return fail(RA_ERR_INVALID_ARG, "the cache overlaps an input");
+  int sms = 0;
+  if ((st = device_info(&sms)) != RA_OK) return st;
+  ra::Kv4CopyParams prm = {};
+  prm.k = k;
+  prm.v = v;
+  prm.k_stride = k_stride;
+  prm.v_stride = v_stride;
+  prm.slots = slots;
+  prm.cache = static_cast<uint8_t*>(cache);
+  prm.T = T;
+  prm.num_slots = static_cast<long long>(num_pages) * page;
+  prm.Hkv = Hkv;
+  prm.page = page;
+  cudaError_t e = ra::launch_kv4_append(prm, d, dtype, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(RA_ERR_CUDA, "append launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+ra_status ring_attn_kv4_read(const void* cache, const int32_t* slots, void* k, void* v, int64_t T,
+                             int Hkv, int d, int dtype, int num_pages, int page,
+                             ra_stream_t stream) {
+  ra_status st = check_kv4_cache(Hkv, d, num_pages, page);
+  if (st != RA_OK) return st;
+  if (T < 0 || T >= (1ll << 31)) return fail(RA_ERR_INVALID_ARG, "T must be in [0, 2^31)");
+  if (dtype != RA_BF16 && dtype != RA_FP16 && dtype != RA_FP32)
+    return fail(RA_ERR_UNSUPPORTED, "dtype %d (supported: RA_BF16, RA_FP16, RA_FP32)", dtype);
+  if (T == 0) return ok();
+  if (!k || !v || !slots || !cache) return fail(RA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(k) || !aligned16(v) || !aligned16(cache) || !aligned4(slots))
+    return fail(RA_ERR_INVALID_ARG, "k, v and cache must be 16-byte aligned, slots 4-byte aligned");
+  const size_t nc = kv4_cache_bytes(Hkv, d, num_pages, page);
+  const size_t no = static_cast<size_t>(T) * Hkv * d * (dtype == RA_FP32 ? 4 : 2);
+  const size_t ns = static_cast<size_t>(T) * 4;
+  if ((nc != 0 && (overlaps(cache, nc, k, no) || overlaps(cache, nc, v, no))) ||
+      overlaps(slots, ns, k, no) || overlaps(slots, ns, v, no) || overlaps(k, no, v, no))
+    return fail(RA_ERR_INVALID_ARG, "outputs overlap the inputs or each other");
+  int sms = 0;
+  if ((st = device_info(&sms)) != RA_OK) return st;
+  ra::Kv4CopyParams prm = {};
+  prm.k_out = k;
+  prm.v_out = v;
+  prm.slots = slots;
+  prm.cache = static_cast<uint8_t*>(const_cast<void*>(cache));
+  prm.T = T;
+  prm.num_slots = static_cast<long long>(num_pages) * page;
+  prm.Hkv = Hkv;
+  prm.page = page;
+  cudaError_t e = ra::launch_kv4_read(prm, d, dtype, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(RA_ERR_CUDA, "read launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+ra_status ring_attn_kv4_workspace_size(size_t* bytes) {
+  if (!bytes) return fail(RA_ERR_INVALID_ARG, "null size pointer");
+  *bytes = ra::KV4_WORKSPACE_BYTES;
+  return ok();
+}
+
+ra_status ring_attn_kv4_fwd(const void* q, int64_t q_stride, const void* cache,
+                            const int32_t* table, const int32_t* lens, const int32_t* cu,
+                            void* out, float* lse, int64_t T, int R, int Hq, int Hkv, int d, int W,
+                            int num_pages, int page, int max_q, int causal, float scale, int dtype,
+                            int out_dtype, void* workspace, size_t workspace_bytes,
+                            ra_stream_t stream) {
+  ra_status st = check_kv4_cache(Hkv, d, num_pages, page);
+  if (st != RA_OK) return st;
+  if (T < 0 || T >= (1ll << 31) || R < 0)
+    return fail(RA_ERR_INVALID_ARG, "T must be in [0, 2^31) and R >= 0 (T=%lld R=%d)",
+                static_cast<long long>(T), R);
+  if (Hq < 1 || Hq % Hkv != 0)
+    return fail(RA_ERR_INVALID_ARG, "Hq=%d is not a positive multiple of Hkv=%d", Hq, Hkv);
+  if (W < 1 || static_cast<long long>(W) * page > (1ll << 30))
+    return fail(RA_ERR_INVALID_ARG, "W must be >= 1 and W * page <= 2^30 (W=%d)", W);
+  if (max_q < 0) return fail(RA_ERR_INVALID_ARG, "max_q must be >= 0 (got %d)", max_q);
+  if (causal != 0 && causal != 1) return fail(RA_ERR_INVALID_ARG, "causal must be 0 or 1");
+  if (!std::isfinite(scale) || scale < 0.f)
+    return fail(RA_ERR_INVALID_ARG, "scale must be finite and >= 0");
+  if (dtype != RA_BF16 && dtype != RA_FP16)
+    return fail(RA_ERR_UNSUPPORTED, "dtype %d (supported: RA_BF16, RA_FP16)", dtype);
+  if (out_dtype != dtype && out_dtype != RA_FP32)
+    return fail(RA_ERR_UNSUPPORTED, "out_dtype must be q's or RA_FP32 (got %d)", out_dtype);
+  const int64_t width = static_cast<int64_t>(Hq) * d;
+  if (static_cast<double>(T) * (Hq / Hkv) >= 2147483648.0)
+    return fail(RA_ERR_INVALID_ARG, "T * Hq / Hkv must be < 2^31");
+  if (q_stride < width || q_stride % 8 != 0)
+    return fail(RA_ERR_INVALID_ARG, "q's token stride must be a multiple of 8 and >= Hq * d");
+  if (!cu && T != R)
+    return fail(RA_ERR_INVALID_ARG, "without cu every request has one query token (T=%lld R=%d)",
+                static_cast<long long>(T), R);
+  if (T == 0 || R == 0) return ok();
+  if (!q || !cache || !table || !lens || !out || !lse || !workspace)
+    return fail(RA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || !aligned16(workspace))
+    return fail(RA_ERR_INVALID_ARG, "q, cache, out and workspace must be 16-byte aligned");
+  if (!aligned4(table) || !aligned4(lens) || !aligned4(cu) || !aligned4(lse))
+    return fail(RA_ERR_INVALID_ARG, "table, lens, cu and lse must be 4-byte aligned");
+  if (workspace_bytes < ra::KV4_WORKSPACE_BYTES)
+    return fail(RA_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu needed",
+                workspace_bytes, ra::KV4_WORKSPACE_BYTES);
+  const size_t nR = static_cast<size_t>(R) * 4;
+  const void* ins[5] = {q, cache, table, lens, cu};
+  const size_t in_n[5] = {span_bytes(T, width, q_stride, 2), kv4_cache_bytes(Hkv, d, num_pages, page),
+                          nR * W, nR, cu ? nR + 4 : 0};
+  const void* outs[3] = {out, lse, workspace};
+  const size_t out_n[3] = {static_cast<size_t>(T) * width * (out_dtype == RA_FP32 ? 4 : 2),
+                           static_cast<size_t>(T) * Hq * 4, ra::KV4_WORKSPACE_BYTES};
+  for (int o = 0; o < 3; ++o) {
+    for (int i = 0; i < 5; ++i)
+      if (in_n[i] != 0 && overlaps(outs[o], out_n[o], ins[i], in_n[i]))
+        return fail(RA_ERR_INVALID_ARG, "an output or the workspace overlaps an input");
+    for (int i = 0; i < o; ++i)
+      if (overlaps(outs[o], out_n[o], outs[i], out_n[i]))
+        return fail(RA_ERR_INVALID_ARG, "outputs and workspace overlap each other");
+  }
+  int sms = 0;
+  if ((st = device_info(&sms)) != RA_OK) return st;
+  ra::Kv4AttnParams prm;
+  std::memset(&prm, 0, sizeof(prm));
+  prm.q = q;
+  prm.q_stride = q_stride;
+  prm.out = out;
+  prm.lse = lse;
+  prm.cache = static_cast<const uint8_t*>(cache);
+  prm.table = table;
+  prm.lens = lens;
+  prm.cu = cu;
+  prm.T = static_cast<int>(T);
+  prm.R = R;
+  prm.Hq = Hq;
+  prm.Hkv = Hkv;
+  prm.group = Hq / Hkv;
+  prm.W = W;
+  prm.page = page;
+  prm.num_pages = num_pages;
+  prm.causal = causal;
+  prm.q_f16 = dtype == RA_FP16;
+  prm.out_f32 = out_dtype == RA_FP32;
+  prm.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  prm.counters = static_cast<unsigned*>(workspace);
+  prm.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + ra::KV4_MAX_CTAS * 4);
+  prm.wait_limit_ns = g_wait_limit_ns.load();
+  const long long rows =
+      static_cast<long long>(cu ? (max_q < prm.T ? max_q : prm.T) : 1) * prm.group;
+  cudaError_t e = ra::launch_kv4_decode(prm, d, rows > 1 << 20 ? 1 << 20 : static_cast<int>(rows),
+                                        sms, g_max_ctas.load(),
+                                        reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(RA_ERR_CUDA, "cache attention launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
 ra_status ring_attn_check_status(ra_stream_t stream) {
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(RA_ERR_CUDA, "stream synchronize: %s", cudaGetErrorString(e));
@@ -670,13 +908,22 @@ ra_status ring_attn_check_status(ra_stream_t stream) {
   e = ra::read_and_clear_status(&v);
   if (e == cudaSuccess) e = ra::read_and_clear_bwd_status(&vb);
   if (e == cudaSuccess) e = ra::read_and_clear_fp8_status(&v8);
+  unsigned long long vc = 0, vd = 0;
+  if (e == cudaSuccess) e = ra::read_and_clear_kv4_cache_status(&vc);
+  if (e == cudaSuccess) e = ra::read_and_clear_kv4_decode_status(&vd);
   if (e != cudaSuccess) return fail(RA_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
   if (v == 0) v = vb;
   if (v == 0) v = v8;
+  if (v == 0) v = vc;
+  if (v == 0) v = vd;
   if (v == 0) return ok();
   const unsigned code = static_cast<unsigned>(v >> 32);
   const unsigned site = static_cast<unsigned>((v >> 16) & 0xFFFF);
   const unsigned cta = static_cast<unsigned>(v & 0xFFFF);
+  if (code == RA_ERR_INVALID_ARG)
+    return fail(RA_ERR_INVALID_ARG,
+                "a slot, page index, length or row start in device memory is out of range "
+                "(site %u, CTA %u)", site, cta);
   return fail(static_cast<ra_status>(code), "device wait ran out (site %u, CTA %u)", site, cta);
 }
 

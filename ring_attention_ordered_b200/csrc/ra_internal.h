@@ -152,6 +152,64 @@ cudaError_t read_and_clear_fp8_status(unsigned long long* out);
 cudaError_t launch_quantize_fp8(const __nv_bfloat16* x, uint8_t* codes, float* scales, int B,
                                 long long L, int H, int d, cudaStream_t stream);
 
+// ---- the paged 4-bit K/V cache (layout and format: ra_kv4.cuh)
+struct Kv4PlanParams {
+  const int32_t* lens;    // [R] tokens held by each request
+  const int32_t* add;     // [R] tokens to add, -1: the request is done
+  const int32_t* table;   // [R, W]
+  const int32_t* pool;    // [num_pages + 1] stack of free pages, its size first
+  int32_t* lens_out;
+  int32_t* table_out;
+  int32_t* pool_out;
+  int32_t* cu;            // [R + 1]
+  int32_t* slots;         // [max_tokens]
+  int32_t* shortage;      // [1]
+  int R, W, num_pages, page;
+  long long max_tokens;
+};
+// Append (k, v -> cache) and read (cache -> k_out, v_out) of the tokens at `slots`.
+struct Kv4CopyParams {
+  const void* k;          // [T, Hkv, d], tokens k_stride elements apart
+  const void* v;
+  long long k_stride, v_stride;
+  void* k_out;            // [T, Hkv, d]
+  void* v_out;
+  const int32_t* slots;   // [T], -1: none
+  uint8_t* cache;
+  long long T, num_slots; // num_slots = num_pages * page
+  int Hkv, page;
+};
+// Attention of the query tokens of R requests over their cached tokens.
+struct Kv4AttnParams {
+  const void* q;          // [T, Hq, d], tokens q_stride elements apart
+  long long q_stride;
+  void* out;              // [T, Hq, d] of q's type, or fp32
+  float* lse;             // [T, Hq]
+  const uint8_t* cache;
+  const int32_t* table;   // [R, W]
+  const int32_t* lens;    // [R]
+  const int32_t* cu;      // [R + 1], or NULL: one query token a request
+  int T, R, Hq, Hkv, group, W, page, num_pages, causal;
+  int q_f16, out_f32;
+  float scale_log2;       // scale * log2(e)
+  unsigned* counters;     // workspace: zero before and after the launch
+  float* partials;        // workspace
+  unsigned long long wait_limit_ns;
+};
+cudaError_t launch_kv4_plan(const Kv4PlanParams& p, cudaStream_t stream);
+cudaError_t launch_kv4_append(const Kv4CopyParams& p, int d, int dtype, cudaStream_t stream);
+cudaError_t launch_kv4_read(const Kv4CopyParams& p, int d, int dtype, cudaStream_t stream);
+cudaError_t read_and_clear_kv4_cache_status(unsigned long long* out);
+cudaError_t launch_kv4_decode(const Kv4AttnParams& p, int d, int rows, int num_sms, int max_ctas,
+                              cudaStream_t stream);
+cudaError_t read_and_clear_kv4_decode_status(unsigned long long* out);
+// Workspace of kv4 attention: counters, then partial results of the pieces
+// into which the launch cuts the work (two a CTA).
+constexpr int KV4_MAX_CTAS = 1024;
+constexpr int KV4_PIECE_FLOATS = 16 * (128 + 2);
+constexpr size_t KV4_WORKSPACE_BYTES =
+    KV4_MAX_CTAS * 4 + 2ull * KV4_MAX_CTAS * KV4_PIECE_FLOATS * 4;
+
 cudaError_t launch_round_bf16(const float* src, __nv_bfloat16* dst, long long n, int num_sms,
                               cudaStream_t stream);
 

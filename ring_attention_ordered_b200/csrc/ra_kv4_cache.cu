@@ -1,0 +1,460 @@
+// The paged 4-bit K/V cache (sm_100a): the page plan, the append and the
+// read.  Layout and format: ra_kv4.cuh.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "ra_internal.h"
+#include "ra_kv4.cuh"
+
+namespace ra {
+namespace {
+
+namespace cg = cooperative_groups;
+
+__device__ unsigned long long g_kv4_cache_status = 0ull;
+
+// ------------------------------------------------------------------ plan
+// Block tables and slot maps from request lengths.  Every CTA of the
+// launch's one cluster computes the same prefix sums over the requests (new
+// tokens, pages that come back, pages that are needed) in shared memory;
+// the lists they number -- released pages, new pages, tokens -- are then
+// dealt out over the cluster's threads.  Three cluster barriers order the
+// phases: everything old has been read before anything is overwritten (the
+// outputs may be the inputs), released pages are on the stack before they
+// are taken again, the table is complete before the slots read it.  The
+// stack positions follow from the prefix sums alone, so the result does not
+// depend on which thread does what.
+constexpr int PLAN_THREADS = 512;
+
+struct PlanSums {
+  long long tok;   // new tokens
+  int rel;         // released pages
+  int take;        // new pages
+};
+
+__device__ __forceinline__ PlanSums operator+(const PlanSums& a, const PlanSums& b) {
+  return {a.tok + b.tok, a.rel + b.rel, a.take + b.take};
+}
+__device__ __forceinline__ PlanSums shfl_up(const PlanSums& a, int n) {
+  return {__shfl_up_sync(0xffffffffu, a.tok, n), __shfl_up_sync(0xffffffffu, a.rel, n),
+          __shfl_up_sync(0xffffffffu, a.take, n)};
+}
+
+// The last index r in [0, n) with pre[r] <= i (pre ascending, pre[0] = 0).
+__device__ __forceinline__ int find_request(const int* pre, int n, int i) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= i) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(PLAN_THREADS) ra_kv4_plan_kernel(const Kv4PlanParams p) {
+  cg::cluster_group cluster = cg::this_cluster();
+  extern __shared__ int plan_smem[];
+  const int R = p.R;
+  int* s_cu = plan_smem;             // [R + 1] new tokens before request r
+  int* s_rel = s_cu + R + 1;         // [R + 1] released pages before request r
+  int* s_take = s_rel + R + 1;       // [R + 1] new pages before request r
+  int* s_len = s_take + R + 1;       // [R]     tokens held before the call
+  __shared__ PlanSums s_warp[PLAN_THREADS / 32];
+  __shared__ PlanSums s_carry;
+  __shared__ int s_bad;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gtid = blockIdx.x * PLAN_THREADS + tid;
+  const int gsize = gridDim.x * PLAN_THREADS;
+  const int n_free = p.pool[0];
+  if (tid == 0) {
+    s_carry = {0, 0, 0};
+    s_bad = n_free < 0 || n_free > p.num_pages;
+  }
+  __syncthreads();
+
+  const long long room = static_cast<long long>(p.W) * p.page;
+  for (int r0 = 0; r0 < R; r0 += PLAN_THREADS) {
+    const int r = r0 + tid;
+    PlanSums x{0, 0, 0};
+    int len = 0;
+    if (r < R) {
+      len = p.lens[r];
+      const int add = p.add[r];
+      const bool bad = len < 0 || add < -1 || len > room || (add > 0 && add > room - len);
+      if (bad) {
+        s_bad = 1;
+        len = 0;
+      } else {
+        const int old = static_cast<int>((static_cast<long long>(len) + p.page - 1) / p.page);
+        if (add < 0) {
+          x.rel = old;
+        } else {
+          x.tok = add;
+          x.take = static_cast<int>((static_cast<long long>(len) + add + p.page - 1) / p.page) - old;
+        }
+      }
+      s_len[r] = len;
+    }
+    PlanSums inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const PlanSums y = shfl_up(inc, o);
+      if (lane >= o) inc = inc + y;
+    }
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    PlanSums base = s_carry;
+    for (int w = 0; w < warp; ++w) base = base + s_warp[w];
+    const PlanSums end = base + inc;
+    if (r < R) {
+      // totals above the limits are refused below; the stored value is then unused
+      s_cu[r + 1] = static_cast<int>(end.tok);
+      s_rel[r + 1] = end.rel;
+      s_take[r + 1] = end.take;
+    }
+    __syncthreads();
+    if (tid == PLAN_THREADS - 1) s_carry = end;
+    __syncthreads();
+  }
+  if (tid == 0) s_cu[0] = s_rel[0] = s_take[0] = 0;
+  __syncthreads();
+  const PlanSums all = s_carry;
+  const bool bad = s_bad != 0 || all.tok > p.max_tokens ||
+                   static_cast<long long>(n_free) + all.rel > p.num_pages;
+  const long long top = bad ? 0 : static_cast<long long>(n_free) + all.rel;
+  const long long missing = bad ? -1 : (all.take > top ? all.take - top : 0);
+  const bool keep = missing != 0;   // nothing changes
+  const int n_rel = keep ? 0 : all.rel, n_take = keep ? 0 : all.take;
+  const int n_tok = keep ? 0 : static_cast<int>(all.tok);
+  const int itop = keep ? n_free : static_cast<int>(top);
+  const int left = itop - n_take;   // free pages after the call
+
+  cluster.sync();   // every CTA has read lens, add and pool[0]
+
+  if (p.table_out != p.table)
+    for (long long i = gtid; i < static_cast<long long>(R) * p.W; i += gsize)
+      p.table_out[i] = p.table[i];
+  if (p.pool_out != p.pool) {
+    const int n_copy = keep ? p.num_pages : min(left, n_free);
+    for (int i = 1 + gtid; i <= n_copy; i += gsize) p.pool_out[i] = p.pool[i];
+  }
+  if (!keep) {
+    // above the stack's new top nothing is left
+    for (int i = itop + 1 + gtid; i <= p.num_pages; i += gsize) p.pool_out[i] = -1;
+  }
+  for (int i = gtid; i < n_rel; i += gsize) {
+    const int r = find_request(s_rel, R + 1, i);
+    p.pool_out[n_free + 1 + i] = p.table[static_cast<long long>(r) * p.W + (i - s_rel[r])];
+  }
+  for (int r = gtid; r < R; r += gsize) {
+    p.cu[r] = keep ? 0 : s_cu[r];
+    const bool done = s_rel[r + 1] != s_rel[r] || p.add[r] < 0;
+    p.lens_out[r] = keep ? p.lens[r] : done ? 0 : s_len[r] + (s_cu[r + 1] - s_cu[r]);
+  }
+  if (gtid == 0) {
+    p.cu[R] = n_tok;
+    p.shortage[0] = static_cast<int>(missing);
+  }
+
+  cluster.sync();   // the released pages are on the stack, the table is copied
+
+  if (gtid == 0) p.pool_out[0] = keep ? n_free : left;
+  for (int i = gtid; i < n_rel; i += gsize) {
+    const int r = find_request(s_rel, R + 1, i);
+    p.table_out[static_cast<long long>(r) * p.W + (i - s_rel[r])] = -1;
+  }
+  for (int i = gtid; i < n_take; i += gsize) {
+    const int r = find_request(s_take, R + 1, i);
+    const int at = itop - i;        // from the top of the stack
+    const int page = at <= n_free ? __ldcg(p.pool + at) : __ldcg(p.pool_out + at);
+    const int old = (s_len[r] + p.page - 1) / p.page;
+    p.table_out[static_cast<long long>(r) * p.W + old + (i - s_take[r])] = page;
+    p.pool_out[at] = -1;
+  }
+
+  cluster.sync();   // the table is complete
+
+  for (long long i = gtid; i < p.max_tokens; i += gsize) {
+    int slot = -1;
+    if (i < n_tok) {
+      const int r = find_request(s_cu, R + 1, static_cast<int>(i));
+      const int pos = s_len[r] + (static_cast<int>(i) - s_cu[r]);
+      slot = __ldcg(p.table_out + static_cast<long long>(r) * p.W + pos / p.page) * p.page +
+             pos % p.page;
+    }
+    p.slots[i] = slot;
+  }
+}
+
+// ------------------------------------------------------------------ append
+template <class T>
+struct Pair;
+template <>
+struct Pair<__nv_bfloat16> {
+  using T2 = __nv_bfloat162;
+  static __device__ __forceinline__ float2 to_float(T2 x) { return __bfloat1622float2(x); }
+};
+template <>
+struct Pair<__half> {
+  using T2 = __half2;
+  static __device__ __forceinline__ float2 to_float(T2 x) { return __half22float2(x); }
+};
+
+template <class T2>
+__device__ __forceinline__ T2 as_pair(uint32_t x) {
+  return *reinterpret_cast<T2*>(&x);
+}
+template <class T2>
+__device__ __forceinline__ uint32_t as_word(T2 x) {
+  return *reinterpret_cast<uint32_t*>(&x);
+}
+
+// The code of one value: the nearest level of 0..15 to (x - zero) / step,
+// ties to the even code.  The quotient by the rounded reciprocal is within
+// 4 ulp of 16 (2^-18) of the exact one, so only a value within 2^-16 of a
+// border can fall on the wrong side; those compare x with the border
+// zero + (n + 1/2) step, which is exact in fp64 (multiples of 2^-25 below
+// 2^17).
+__device__ __forceinline__ uint32_t kv4_code(float x, float zero, float step, float inv) {
+  const float t = fminf(fmaxf((x - zero) * inv, 0.f), 15.f);
+  const float n = floorf(t);
+  uint32_t c = static_cast<uint32_t>(n);
+  const float f = t - n;
+  if (fabsf(f - 0.5f) < 1.52587890625e-5f) {
+    const double border = static_cast<double>(zero) +
+                          (static_cast<double>(n) + 0.5) * static_cast<double>(step);
+    const double d = static_cast<double>(x) - border;
+    c += d > 0.0 ? 1u : d == 0.0 ? (c & 1u) : 0u;
+  } else {
+    c += f > 0.5f ? 1u : 0u;
+  }
+  return c;
+}
+
+// Eight values of one lane; the LANES lanes of the vector agree on its range.
+// Returns the codes (element i in nibble i) and the parameter word.
+template <class T, int LANES>
+__device__ __forceinline__ uint2 kv4_encode8(uint4 x) {
+  using T2 = typename Pair<T>::T2;
+  const T2 a = as_pair<T2>(x.x), b = as_pair<T2>(x.y), c = as_pair<T2>(x.z), d = as_pair<T2>(x.w);
+  const T2 mn = __hmin2_nan(__hmin2_nan(a, b), __hmin2_nan(c, d));
+  const T2 mx = __hmax2_nan(__hmax2_nan(a, b), __hmax2_nan(c, d));
+  // (min, -max) in one word: both are minima, exact in the input's type
+  const uint32_t mnw = as_word<T2>(mn), mxw = as_word<T2>(mx) ^ 0x80008000u;
+  T2 m = __hmin2_nan(as_pair<T2>(__byte_perm(mnw, mxw, 0x5410)),
+                     as_pair<T2>(__byte_perm(mnw, mxw, 0x7632)));
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1)
+    m = __hmin2_nan(m, as_pair<T2>(__shfl_xor_sync(0xffffffffu, as_word<T2>(m), o)));
+  const float2 r = Pair<T>::to_float(m);
+  const bool nan = r.x != r.x;   // a NaN reaches both halves
+  const float lo = fminf(fmaxf(r.x, -65504.f), 65504.f);
+  const float hi = fminf(fmaxf(-r.y, -65504.f), 65504.f);
+  const __half zh = __float2half_rn(lo);
+  __half sh = __float2half_rz(__fdiv_rn(hi - lo, 15.f));
+  if (__half_as_ushort(sh) == 0) sh = __ushort_as_half(1);
+  const float zero = __half2float(zh), step = __half2float(sh);
+  const float inv = __frcp_rn(step);
+  uint32_t codes = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = Pair<T>::to_float(as_pair<T2>(i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w));
+    codes |= kv4_code(v.x, zero, step, inv) << (8 * i);
+    codes |= kv4_code(v.y, zero, step, inv) << (8 * i + 4);
+  }
+  const uint32_t params = nan ? 0x7FFF7FFFu
+                              : static_cast<uint32_t>(__half_as_ushort(sh)) |
+                                    (static_cast<uint32_t>(__half_as_ushort(zh)) << 16);
+  return make_uint2(nan ? 0u : codes, params);
+}
+
+// Work items of append and read: one (token, head) to LANES = d / 8 lanes of
+// 8 elements.  Items run over the tokens of a group of 16 first, then over
+// the heads, so that the two tokens whose V codes share a sector are handled
+// by neighbouring lanes.
+constexpr int CACHE_THREADS = 256;
+
+struct Item {
+  long long token;
+  int head;
+};
+__device__ __forceinline__ Item item_of(long long i, int Hkv) {
+  const long long group = i / (16 * Hkv);
+  const int rest = static_cast<int>(i - group * (16 * Hkv));
+  return {group * 16 + (rest & 15), rest >> 4};
+}
+
+template <int D, class T>
+__global__ void __launch_bounds__(CACHE_THREADS) ra_kv4_append_kernel(const Kv4CopyParams p) {
+  using L = Kv4<D>;
+  constexpr int LANES = D / 8;
+  const long long tid = static_cast<long long>(blockIdx.x) * CACHE_THREADS + threadIdx.x;
+  const Item it = item_of(tid / LANES, p.Hkv);
+  const int j = static_cast<int>(tid % LANES);
+  const bool in = it.token < p.T && it.head < p.Hkv;
+  long long slot = in ? p.slots[it.token] : -1;
+  if (slot >= p.num_slots || slot < -1) {
+    kv4_record(&g_kv4_cache_status, RA_ERR_INVALID_ARG, KV4_SITE_SLOT);
+    slot = -1;
+  }
+  const bool use = slot >= 0;
+  uint4 k = make_uint4(0, 0, 0, 0), v = k;
+  if (use) {
+    k = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.k) + it.token * p.k_stride +
+                                        it.head * D + j * 8);
+    v = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + it.token * p.v_stride +
+                                        it.head * D + j * 8);
+  }
+  const uint2 kc = kv4_encode8<T, LANES>(k);
+  const uint2 vc = kv4_encode8<T, LANES>(v);
+  if (!use) return;
+  const long long page = slot / p.page;
+  const int o = static_cast<int>(slot - page * p.page);
+  const int i = o & 15;
+  uint8_t* blk = p.cache + ((page * p.Hkv + it.head) * (p.page >> 4) + (o >> 4)) * L::BLOCK_BYTES;
+  *reinterpret_cast<uint32_t*>(blk + i * L::ROW + j * 4) = kc.x;
+  uint8_t* vb = blk + L::OFF_V;
+  *reinterpret_cast<uint16_t*>(vb + L::v_code_offset(i, 2 * j)) = static_cast<uint16_t>(vc.x);
+  *reinterpret_cast<uint16_t*>(vb + L::v_code_offset(i, 2 * j + 1)) =
+      static_cast<uint16_t>(vc.x >> 16);
+  if (j == 0) {
+    *reinterpret_cast<uint32_t*>(blk + L::OFF_KP + 4 * i) = kc.y;
+    *reinterpret_cast<uint32_t*>(blk + L::OFF_VP + 4 * i) = vc.y;
+  }
+}
+
+// ------------------------------------------------------------------ read
+__device__ __forceinline__ void store8(float* dst, const float (&x)[8]) {
+  reinterpret_cast<float4*>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* dst, const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = as_word<__nv_bfloat162>(__floats2bfloat162_rn(x[2 * i], x[2 * i + 1]));
+  *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(__half* dst, const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = as_word<__half2>(__floats2half2_rn(x[2 * i], x[2 * i + 1]));
+  *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <class T>
+__device__ __forceinline__ void decode8(T* dst, uint32_t codes, uint32_t params, bool use) {
+  const float2 sz = kv4_params(params);
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    x[i] = use ? fmaf(sz.x, static_cast<float>((codes >> (4 * i)) & 15u), sz.y) : 0.f;
+  store8(dst, x);
+}
+
+template <int D, class T>
+__global__ void __launch_bounds__(CACHE_THREADS) ra_kv4_read_kernel(const Kv4CopyParams p) {
+  using L = Kv4<D>;
+  constexpr int LANES = D / 8;
+  const long long tid = static_cast<long long>(blockIdx.x) * CACHE_THREADS + threadIdx.x;
+  const Item it = item_of(tid / LANES, p.Hkv);
+  const int j = static_cast<int>(tid % LANES);
+  if (it.token >= p.T || it.head >= p.Hkv) return;
+  long long slot = p.slots[it.token];
+  if (slot >= p.num_slots || slot < -1) {
+    kv4_record(&g_kv4_cache_status, RA_ERR_INVALID_ARG, KV4_SITE_SLOT);
+    slot = -1;
+  }
+  const bool use = slot >= 0;
+  uint32_t kc = 0, vc = 0, kp = 0, vp = 0;
+  if (use) {
+    const long long page = slot / p.page;
+    const int o = static_cast<int>(slot - page * p.page);
+    const int i = o & 15;
+    const uint8_t* blk =
+        p.cache + ((page * p.Hkv + it.head) * (p.page >> 4) + (o >> 4)) * L::BLOCK_BYTES;
+    kc = *reinterpret_cast<const uint32_t*>(blk + i * L::ROW + j * 4);
+    const uint8_t* vb = blk + L::OFF_V;
+    vc = *reinterpret_cast<const uint16_t*>(vb + L::v_code_offset(i, 2 * j)) |
+         (static_cast<uint32_t>(
+              *reinterpret_cast<const uint16_t*>(vb + L::v_code_offset(i, 2 * j + 1)))
+          << 16);
+    kp = *reinterpret_cast<const uint32_t*>(blk + L::OFF_KP + 4 * i);
+    vp = *reinterpret_cast<const uint32_t*>(blk + L::OFF_VP + 4 * i);
+  }
+  const long long dst = (it.token * p.Hkv + it.head) * D + j * 8;
+  decode8(static_cast<T*>(p.k_out) + dst, kc, kp, use);
+  decode8(static_cast<T*>(p.v_out) + dst, vc, vp, use);
+}
+
+template <class F>
+cudaError_t launch_copy(F kernel, const Kv4CopyParams& p, int d, cudaStream_t stream) {
+  const long long groups = (p.T + 15) / 16;
+  const long long threads = groups * 16 * p.Hkv * (d / 8);
+  const long long grid = (threads + CACHE_THREADS - 1) / CACHE_THREADS;
+  if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  kernel<<<static_cast<unsigned>(grid), CACHE_THREADS, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_plan(const Kv4PlanParams& p, cudaStream_t stream) {
+  const size_t smem = static_cast<size_t>(4 * p.R + 3) * sizeof(int);
+  cudaError_t e = cudaSuccess;
+  if (smem > 40 * 1024) {
+    e = cudaFuncSetAttribute(ra_kv4_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  // One CTA for what one CTA's threads do in a few rounds, else a cluster.
+  long long work = p.max_tokens;
+  if (p.table_out != p.table) work += static_cast<long long>(p.R) * p.W;
+  if (p.pool_out != p.pool) work += p.num_pages;
+  const unsigned ctas = work <= 8 * PLAN_THREADS ? 1 : 8;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(PLAN_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ctas;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, ra_kv4_plan_kernel, p);
+}
+
+cudaError_t launch_kv4_append(const Kv4CopyParams& p, int d, int dtype, cudaStream_t stream) {
+  if (dtype == RA_BF16)
+    return d == 128 ? launch_copy(ra_kv4_append_kernel<128, __nv_bfloat16>, p, d, stream)
+                    : launch_copy(ra_kv4_append_kernel<64, __nv_bfloat16>, p, d, stream);
+  return d == 128 ? launch_copy(ra_kv4_append_kernel<128, __half>, p, d, stream)
+                  : launch_copy(ra_kv4_append_kernel<64, __half>, p, d, stream);
+}
+
+cudaError_t launch_kv4_read(const Kv4CopyParams& p, int d, int dtype, cudaStream_t stream) {
+  if (dtype == RA_BF16)
+    return d == 128 ? launch_copy(ra_kv4_read_kernel<128, __nv_bfloat16>, p, d, stream)
+                    : launch_copy(ra_kv4_read_kernel<64, __nv_bfloat16>, p, d, stream);
+  if (dtype == RA_FP16)
+    return d == 128 ? launch_copy(ra_kv4_read_kernel<128, __half>, p, d, stream)
+                    : launch_copy(ra_kv4_read_kernel<64, __half>, p, d, stream);
+  return d == 128 ? launch_copy(ra_kv4_read_kernel<128, float>, p, d, stream)
+                  : launch_copy(ra_kv4_read_kernel<64, float>, p, d, stream);
+}
+
+cudaError_t read_and_clear_kv4_cache_status(unsigned long long* out) {
+  unsigned long long v = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_kv4_cache_status, sizeof(v));
+  if (e == cudaSuccess && v != 0) e = cudaMemcpyToSymbol(g_kv4_cache_status, &zero, sizeof(zero));
+  *out = v;
+  return e;
+}
+
+}  // namespace ra

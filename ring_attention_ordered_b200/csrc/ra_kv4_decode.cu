@@ -1,0 +1,526 @@
+// Attention of a few query rows over the paged 4-bit K/V cache (sm_100a).
+//
+// For every request r, K/V head h and query row (query token t of the
+// request, query head of h's group)
+//     out = sum_c softmax_c(scale q . k_c) v_c,   lse = ln sum_c exp(scale q . k_c)
+// over the cached tokens c the row sees, with k = ks codeK + kz and
+// v = vs codeV + vz (step and zero of each token and head).
+//
+// The codes go to the matrix instructions as they are, and the steps and
+// zeros are applied in fp32 around them, so nothing of K or V is rounded:
+//     q . k   = ks (q . codeK) + kz sum(q)
+//     sum p v = sum (p vs) codeV + sum p vz
+// * A nibble under the mask 0x000f is a subnormal fp16 number, code 2^-24,
+//   and under 0x00f0 it is code 2^-20: two codes become an operand register
+//   with one AND (and one shift for every second pair), no conversion.  The
+//   factor 16 between them is taken back in q (K: both lie in the sum over d,
+//   q there is divided by 16) and in the result (V: they are different rows
+//   of it).
+// * q is scaled by a power of two per row so that its largest value lies in
+//   [2^14, 2^15): exact in fp16 for bf16 and fp16 inputs down to 2^-24 of the
+//   row's maximum.
+// * p vs = 2^(s - m + 8) vs is rounded to fp16 (2^-12 relative, finer than the
+//   output type) for the product with the codes; the row sum and the sum of
+//   p vz use the fp32 values.  m is any reference that keeps p vs below
+//   2^15: it is moved, and the accumulators rescaled, only when a value of the
+//   block in hand would pass that, which one vote per block finds out.  The
+//   step is part of what is bounded, so m follows max(s + log2 vs).
+//
+// Work: S^T = K q^T and O^T = V^T P^T with mma m16n8k16: a block of 16 tokens
+// is the M side, 8 query rows (NT tiles of them) the N side, so the padding of
+// a small group costs idle columns, not tensor time.  The transposition of P
+// between the products is one movmatrix per 8 tokens.  Each warp streams
+// blocks of its own through a private ring of shared-memory stages (one bulk
+// copy a block: block i of the warp is refilled as soon as its words are in
+// registers); the warps of a CTA take every 8th block of the CTA's piece and
+// are merged at its end.
+//
+// Split: the blocks of all (request, head, row tile) units form one line,
+// request-major, and the CTAs take equal stretches of it, so a long request is spread
+// over the GPU and short ones are packed, whatever the lengths, which only
+// the device knows.  A unit that crosses stretches is merged by the CTA that
+// finishes last (a counter that it sets back to zero), over the pieces in
+// their order, so the result does not depend on the order of arrival.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "ptx_sm100.cuh"
+#include "ra_internal.h"
+#include "ra_kv4.cuh"
+#include "ra_kv4_attn.cuh"
+#include "ra_sync.cuh"
+
+namespace ra {
+namespace kv4d {
+
+constexpr int WARPS = 8;
+constexpr int THREADS = WARPS * 32;
+constexpr int STAGES = 4;
+constexpr int MIN_BLOCKS = 32;     // blocks below which a stretch is not cut further
+constexpr float P_SHIFT = 8.f;     // p vs = 2^P_SHIFT at the reference
+constexpr float P_LIMIT = 32768.f;
+
+__device__ unsigned long long g_status = 0ull;
+
+template <int D, int NT>
+struct Smem {
+  static constexpr int RING = WARPS * STAGES * Kv4<D>::BLOCK_BYTES;
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int RS = D + 4;                       // row stride of the merge buffer
+  static constexpr int MERGE = WARPS * ROWS * RS * 4;
+  static constexpr int OFF_ML = RING > MERGE ? RING : MERGE;
+  static constexpr int OFF_BAR = OFF_ML + 2 * WARPS * ROWS * 4;
+  static constexpr int BYTES = OFF_BAR + WARPS * STAGES * 8;
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t (&r)[N], uint32_t addr) {
+  static_assert(N == 2 || N == 4, "8 or 16 bytes");
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+  else
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(addr));
+  return r;
+}
+// Nibbles (0, 4), (1, 5), (2, 6), (3, 7) of a word as fp16 pairs: codes times
+// 2^-24, 2^-20, 2^-24, 2^-20.
+__device__ __forceinline__ void code_pairs(uint32_t x, uint32_t (&p)[4]) {
+  const uint32_t y = x >> 8;
+  p[0] = x & 0x000f000fu;
+  p[1] = x & 0x00f000f0u;
+  p[2] = y & 0x000f000fu;
+  p[3] = y & 0x00f000f0u;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
+    ra_kv4_decode_kernel(const Kv4AttnParams p) {
+  using L = Kv4<D>;
+  using S = Smem<D, NT>;
+  constexpr int WPL = D / 32;        // code words of a row per lane (16 or 8 bytes)
+  constexpr int ROWS = 8 * NT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint32_t s_abort;
+  __shared__ int s_last;
+  __shared__ Kv4Start s_start;
+  __shared__ long long s_scan[WARPS + 1];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t ring = smem_u32(smem) + warp * STAGES * L::BLOCK_BYTES;
+  const uint32_t bars = smem_u32(smem) + S::OFF_BAR + warp * STAGES * 8;
+  float* s_merge = reinterpret_cast<float*>(smem);
+  float* s_m = reinterpret_cast<float*>(smem + S::OFF_ML);
+  float* s_l = s_m + WARPS * ROWS;
+  const Ctl cx{&s_abort, p.wait_limit_ns, &g_status};
+
+  if (tid == 0) s_abort = 0u;
+  if (lane == 0) {
+    for (int i = 0; i < STAGES; ++i) mbar_init(bars + 8 * i, 1);
+    fence_mbarrier_init();
+  }
+  kv4_fill_empty<D, THREADS>(p, &g_status);
+  // the stretch of this CTA: [start.at, start.end) of the line of blocks
+  kv4_find_start<ROWS, MIN_BLOCKS, WARPS>(p, KV4_BLOCK, s_scan, s_start);
+  __syncthreads();
+  long long at = s_start.at;
+  const long long end = s_start.end;
+  const long long per_cta = s_start.per_cta;
+  int r = s_start.r;
+  long long in_r = s_start.in_r;     // blocks of request r before `at`
+  uint32_t it = 0;                   // blocks this warp has taken from its ring
+
+  while (at < end) {
+    Kv4Req q = kv4_request(p, r);
+    const int nb = (q.len + KV4_BLOCK - 1) / KV4_BLOCK;
+    const int rows = q.n * p.group;
+    const int tiles = (rows + ROWS - 1) / ROWS;
+    if (in_r >= static_cast<long long>(tiles) * p.Hkv * nb) {
+      ++r;
+      in_r = 0;
+      continue;
+    }
+    const int unit = static_cast<int>(in_r / nb);
+    const int b0 = static_cast<int>(in_r - static_cast<long long>(unit) * nb);
+    const int take = static_cast<int>(min(end - at, static_cast<long long>(nb - b0)));
+    const int b1 = b0 + take;
+    const int h = unit / tiles, row0 = (unit - h * tiles) * ROWS;
+
+    // ---- copies: lane i looks up the warp's blocks i, i + 32, ...
+    const int n_mine = take > warp ? (take - warp + WARPS - 1) / WARPS : 0;
+    int ent = -1;
+    auto lookup = [&](int base) {
+      const int blk = b0 + warp + WARPS * (base + lane);
+      ent = blk < b1 ? kv4_block_index(p, r, h, blk, &g_status) : -1;
+    };
+    auto issue = [&](int i) {   // block i of this warp into stage (it0 + i) % STAGES
+      if ((i & 31) == 0) lookup(i);
+      const int e = __shfl_sync(0xffffffffu, ent, i & 31);
+      if (lane == 0) {
+        const uint32_t s = (it + i) % STAGES;
+        if (e >= 0) {
+          mbar_arrive_expect_tx(bars + 8 * s, L::BLOCK_BYTES);
+          bulk_load(ring + s * L::BLOCK_BYTES,
+                    p.cache + static_cast<long long>(e) * L::BLOCK_BYTES, L::BLOCK_BYTES,
+                    bars + 8 * s);
+        } else {
+          mbar_arrive(bars + 8 * s);
+        }
+      }
+      return e;
+    };
+    uint32_t bad = 0;   // stages whose page is out of range
+    int issued = 0;
+    auto issue_next = [&] {
+      if (issued < n_mine) {
+        const uint32_t bit = 1u << ((it + issued) % STAGES);
+        bad = issue(issued) >= 0 ? (bad & ~bit) : (bad | bit);
+        ++issued;
+      }
+    };
+    const uint32_t it0 = it;
+    for (int i = 0; i < STAGES; ++i) issue_next();
+
+    // ---- q: operand registers, scale and sum of each row
+    uint32_t qf[NT][2 * WPL][2];
+    float rho[NT][2], sigma[NT][2];
+    int lim[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int row = row0 + 8 * j + g;
+      float x[8 * WPL];
+      kv4_load_q<8 * WPL>(p, q, h, row, rows, t * 8 * WPL, D, x);
+      float am = 0.f, sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8 * WPL; ++i) {
+        am = fmaxf(am, fabsf(x[i]));
+        sum += x[i];
+      }
+      am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+      am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      float up, down;
+      kv4_row_scale(am, up, down);
+      float y[8 * WPL];
+#pragma unroll
+      for (int i = 0; i < 8 * WPL; ++i) y[i] = x[i] * up;
+#pragma unroll
+      for (int w = 0; w < WPL; ++w) {
+        const float* e = y + 8 * w;
+        const float k = 0.0625f;
+        qf[j][2 * w][0] = pack_f16x2(e[0], e[4]);
+        qf[j][2 * w][1] = pack_f16x2(e[1] * k, e[5] * k);
+        qf[j][2 * w + 1][0] = pack_f16x2(e[2], e[6]);
+        qf[j][2 * w + 1][1] = pack_f16x2(e[3] * k, e[7] * k);
+      }
+      // columns 2t, 2t + 1 of the product are the rows of lanes 8t, 8t + 4
+      const float ro = down * p.scale_log2, so = sum * p.scale_log2;
+      const int lo = kv4_limit(p, q, row, rows);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int src = (2 * t + c) * 4;
+        rho[j][c] = __shfl_sync(0xffffffffu, ro, src) * 16777216.f;
+        sigma[j][c] = __shfl_sync(0xffffffffu, so, src);
+        lim[j][c] = __shfl_sync(0xffffffffu, lo, src);
+      }
+    }
+    int lim_min = lim[0][0];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) lim_min = min(lim_min, min(lim[j][0], lim[j][1]));
+    lim_min = __reduce_min_sync(0xffffffffu, lim_min);
+
+    float o[NT][2 * WPL][4];
+    float mo[NT][2], l[NT][2], z[NT][2];   // mo = P_SHIFT - m
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int i = 0; i < 2 * WPL; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[j][i][c] = 0.f;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        mo[j][c] = INFINITY;
+        l[j][c] = z[j][c] = 0.f;
+      }
+    }
+
+    bool alive = true;
+    for (int i = 0; i < n_mine; ++i) {
+      const uint32_t s = (it0 + i) % STAGES;
+      if (!wait_warp(bars + 8 * s, ((it0 + i) / STAGES) & 1u, cx, KV4_SITE_COPY)) {
+        alive = false;
+        break;
+      }
+      const bool skip = (bad >> s) & 1u;
+      const uint32_t blk = ring + s * L::BLOCK_BYTES;
+      uint32_t k0[WPL], k1[WPL], v0[WPL], v1[WPL];
+      lds_words(k0, blk + g * L::ROW + t * (4 * WPL));
+      lds_words(k1, blk + (g + 8) * L::ROW + t * (4 * WPL));
+      lds_words(v0, blk + L::OFF_V + lane * (4 * WPL));
+      lds_words(v1, blk + L::OFF_V + 4 * D + lane * (4 * WPL));
+      const uint32_t kp0 = lds32(blk + L::OFF_KP + 4 * g), kp1 = lds32(blk + L::OFF_KP + 4 * g + 32);
+      const uint32_t vp0 = lds32(blk + L::OFF_VP + 4 * g), vp1 = lds32(blk + L::OFF_VP + 4 * g + 32);
+      __syncwarp();
+      issue_next();
+      if (skip) continue;
+
+      float c[NT][4];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) c[j][0] = c[j][1] = c[j][2] = c[j][3] = 0.f;
+#pragma unroll
+      for (int w = 0; w < WPL; ++w) {
+        uint32_t a[4], b[4];
+        code_pairs(k0[w], a);
+        code_pairs(k1[w], b);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          mma_f16(c[j], a[0], b[0], a[1], b[1], qf[j][2 * w][0], qf[j][2 * w][1]);
+          mma_f16(c[j], a[2], b[2], a[3], b[3], qf[j][2 * w + 1][0], qf[j][2 * w + 1][1]);
+        }
+      }
+
+      const float2 ks0 = kv4_params(kp0), ks1 = kv4_params(kp1);
+      const float2 vs0 = kv4_params(vp0), vs1 = kv4_params(vp1);
+      const int key = (b0 + warp + WARPS * i) * KV4_BLOCK + g;
+      const bool tail = (b0 + warp + WARPS * i + 1) * KV4_BLOCK > lim_min;
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        // scores without the reference, log2 units
+        float sc[4];
+        sc[0] = fmaf(c[j][0] * rho[j][0], ks0.x, ks0.y * sigma[j][0]);
+        sc[1] = fmaf(c[j][1] * rho[j][1], ks0.x, ks0.y * sigma[j][1]);
+        sc[2] = fmaf(c[j][2] * rho[j][0], ks1.x, ks1.y * sigma[j][0]);
+        sc[3] = fmaf(c[j][3] * rho[j][1], ks1.x, ks1.y * sigma[j][1]);
+        float e[4], pv[4];
+        auto weights = [&] {
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+            e[q4] = ex2_approx(sc[q4] + mo[j][q4 & 1]);
+            pv[q4] = e[q4] * (q4 < 2 ? vs0.x : vs1.x);
+          }
+          if (tail) {
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4)
+              if (key + (q4 < 2 ? 0 : 8) >= lim[j][q4 & 1]) e[q4] = pv[q4] = 0.f;
+          }
+        };
+        weights();
+        const float top = fmaxf(fmaxf(pv[0], pv[1]), fmaxf(pv[2], pv[3]));
+        const bool nan = pv[0] != pv[0] || pv[1] != pv[1] || pv[2] != pv[2] || pv[3] != pv[3];
+        if (__any_sync(0xffffffffu, nan || top > P_LIMIT)) {
+          // move the reference to the largest s + log2(vs) so far
+          const float lv0 = __log2f(fmaxf(vs0.x, 5.9604645e-8f));
+          const float lv1 = __log2f(fmaxf(vs1.x, 5.9604645e-8f));
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            float w0 = sc[cc] + lv0, w1 = sc[2 + cc] + lv1;
+            if (tail) {
+              if (key >= lim[j][cc]) w0 = -INFINITY;
+              if (key + 8 >= lim[j][cc]) w1 = -INFINITY;
+            }
+            float w = fmaxf(w0, w1);
+            w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 4));
+            w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 8));
+            w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 16));
+            const float mo_new = fminf(mo[j][cc], P_SHIFT - w);
+            const float alpha = mo_new == mo[j][cc] ? 1.f : ex2_approx(mo_new - mo[j][cc]);
+            mo[j][cc] = mo_new;
+            l[j][cc] *= alpha;
+            z[j][cc] *= alpha;
+#pragma unroll
+            for (int i2 = 0; i2 < 2 * WPL; ++i2) {
+              o[j][i2][cc] *= alpha;
+              o[j][i2][2 + cc] *= alpha;
+            }
+          }
+          weights();
+        }
+        l[j][0] += e[0] + e[2];
+        l[j][1] += e[1] + e[3];
+        if (tail) {
+          // a hidden token's parameters may be NaN: 0 times them is not 0
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            if (key < lim[j][cc]) z[j][cc] = fmaf(e[cc], vs0.y, z[j][cc]);
+            if (key + 8 < lim[j][cc]) z[j][cc] = fmaf(e[2 + cc], vs1.y, z[j][cc]);
+          }
+        } else {
+          z[j][0] = fmaf(e[0], vs0.y, fmaf(e[2], vs1.y, z[j][0]));
+          z[j][1] = fmaf(e[1], vs0.y, fmaf(e[3], vs1.y, z[j][1]));
+        }
+        pb[j][0] = transpose8(pack_f16x2(pv[0], pv[1]));
+        pb[j][1] = transpose8(pack_f16x2(pv[2], pv[3]));
+      }
+#pragma unroll
+      for (int w = 0; w < WPL; ++w) {
+        uint32_t a[4], b[4];
+        code_pairs(v0[w], a);
+        code_pairs(v1[w], b);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          mma_f16(o[j][2 * w], a[0], a[1], b[0], b[1], pb[j][0], pb[j][1]);
+          mma_f16(o[j][2 * w + 1], a[2], a[3], b[2], b[3], pb[j][0], pb[j][1]);
+        }
+      }
+    }
+    if (!alive) {
+      // let the copies in flight land before the shared memory goes
+      for (int i = 0; i < issued; ++i)
+        if (i + STAGES >= issued && lane == 0)
+          drain_wait(bars + 8 * ((it0 + i) % STAGES), ((it0 + i) / STAGES) & 1u, 200000000ull);
+      __syncwarp();
+    }
+    it = it0 + n_mine;
+
+    // ---- merge the warps: A = sum p v (relative to m), m, l per row
+    __syncthreads();   // every warp has left its ring, which the buffer overlaps
+    if (s_abort) return;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        float ls = l[j][cc], zs = z[j][cc];
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          ls += __shfl_xor_sync(0xffffffffu, ls, x);
+          zs += __shfl_xor_sync(0xffffffffu, zs, x);
+        }
+        const int row = 8 * j + 2 * t + cc;
+        float* dst = s_merge + (warp * ROWS + row) * S::RS + g * (D / 8);
+#pragma unroll
+        for (int w = 0; w < WPL; ++w)
+          *reinterpret_cast<float4*>(dst + 4 * w) =
+              make_float4(fmaf(o[j][2 * w][cc], 16777216.f, zs),
+                          fmaf(o[j][2 * w][2 + cc], 1048576.f, zs),
+                          fmaf(o[j][2 * w + 1][cc], 16777216.f, zs),
+                          fmaf(o[j][2 * w + 1][2 + cc], 1048576.f, zs));
+        if (g == 0) {
+          s_m[warp * ROWS + row] = P_SHIFT - mo[j][cc];
+          s_l[warp * ROWS + row] = ls;
+        }
+      }
+    __syncthreads();
+
+    const bool whole = b0 == 0 && b1 == nb;
+    // the unit's blocks on the line, and the CTAs whose stretches hold them
+    const long long u0 = at - b0;
+    const int c0 = static_cast<int>(u0 / per_cta);
+    const int c1 = static_cast<int>((u0 + nb - 1) / per_cta);
+    float* slot = p.partials + (2ll * blockIdx.x + (static_cast<int>(blockIdx.x) == c0)) * KV4_PIECE_FLOATS;
+    const int n_rows = min(ROWS, rows - row0);
+    for (int i = tid; i < n_rows * (D / 4); i += THREADS) {
+      const int row = i / (D / 4), d4 = i - row * (D / 4);
+      float m = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) m = fmaxf(m, s_m[w * ROWS + row]);
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      float ls = 0.f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float mw = s_m[w * ROWS + row];
+        const float f = mw == -INFINITY ? 0.f : mw == m ? 1.f : ex2_approx(mw - m);
+        const float4 x = *reinterpret_cast<const float4*>(s_merge + (w * ROWS + row) * S::RS + 4 * d4);
+        if (f != 0.f) {
+          a.x = fmaf(f, x.x, a.x);
+          a.y = fmaf(f, x.y, a.y);
+          a.z = fmaf(f, x.z, a.z);
+          a.w = fmaf(f, x.w, a.w);
+          ls = fmaf(f, s_l[w * ROWS + row], ls);
+        }
+      }
+      if (whole) {
+        kv4_store(p, q, h, row0 + row, 4 * d4, D, a, m - P_SHIFT, ls);
+      } else {
+        *reinterpret_cast<float4*>(slot + row * D + 4 * d4) = a;
+        if (d4 == 0) {
+          slot[ROWS * D + row] = m;
+          slot[ROWS * D + ROWS + row] = ls;
+        }
+      }
+    }
+    if (!whole) {
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const unsigned old = atomicAdd(p.counters + c0, 1u);
+        s_last = old == static_cast<unsigned>(c1 - c0);
+        if (s_last) p.counters[c0] = 0u;
+        __threadfence();
+      }
+      __syncthreads();
+      if (s_last) {
+        for (int i = tid; i < n_rows * (D / 4); i += THREADS) {
+          const int row = i / (D / 4), d4 = i - row * (D / 4);
+          float m = -INFINITY, ls = 0.f;
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int c = c0; c <= c1; ++c) {
+            const float* src = p.partials + (2ll * c + (c == c0)) * KV4_PIECE_FLOATS;
+            kv4_merge(m, ls, a, __ldcg(src + ROWS * D + row), __ldcg(src + ROWS * D + ROWS + row),
+                      __ldcg(reinterpret_cast<const float4*>(src + row * D + 4 * d4)));
+          }
+          kv4_store(p, q, h, row0 + row, 4 * d4, D, a, m - P_SHIFT, ls);
+        }
+      }
+    }
+    fence_proxy_async();
+    __syncthreads();     // the merge buffer is free for copies again
+    at += take;
+    in_r += take;
+  }
+}
+
+template <int D, int NT>
+cudaError_t launch(const Kv4AttnParams& p, int num_sms, int max_ctas, cudaStream_t stream) {
+  using S = Smem<D, NT>;
+  cudaError_t e = cudaFuncSetAttribute(ra_kv4_decode_kernel<D, NT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
+  if (e != cudaSuccess) return e;
+  int grid = num_sms * (NT == 1 ? 2 : 1);
+  if (max_ctas > 0 && max_ctas < grid) grid = max_ctas;
+  if (grid > KV4_MAX_CTAS) grid = KV4_MAX_CTAS;
+  ra_kv4_decode_kernel<D, NT><<<grid, THREADS, S::BYTES, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace kv4d
+
+cudaError_t launch_kv4_decode(const Kv4AttnParams& p, int d, int rows, int num_sms, int max_ctas,
+                              cudaStream_t stream) {
+  if (rows <= 8)
+    return d == 128 ? kv4d::launch<128, 1>(p, num_sms, max_ctas, stream)
+                    : kv4d::launch<64, 1>(p, num_sms, max_ctas, stream);
+  return d == 128 ? kv4d::launch<128, 2>(p, num_sms, max_ctas, stream)
+                  : kv4d::launch<64, 2>(p, num_sms, max_ctas, stream);
+}
+
+cudaError_t read_and_clear_kv4_decode_status(unsigned long long* out) {
+  unsigned long long v = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, kv4d::g_status, sizeof(v));
+  if (e == cudaSuccess && v != 0) e = cudaMemcpyToSymbol(kv4d::g_status, &zero, sizeof(zero));
+  *out = v;
+  return e;
+}
+
+}  // namespace ra
