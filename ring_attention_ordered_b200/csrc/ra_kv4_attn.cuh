@@ -191,24 +191,25 @@ struct Kv4Start {
   int r;
 };
 
-// Blocks of `keys` tokens that request r puts on the line.
-template <int ROWS>
+// Cells that request r takes on the line: for each of its units the blocks of
+// `keys` tokens, and UNIT_COST before them.
+template <int ROWS, int UNIT_COST>
 __device__ __forceinline__ long long kv4_work(const Kv4AttnParams& p, int r, int keys) {
   const Kv4Req q = kv4_request(p, r);
   const int tiles = (q.n * p.group + ROWS - 1) / ROWS;
-  return static_cast<long long>(tiles) * p.Hkv * ((q.len + keys - 1) / keys);
+  const int nb = (q.len + keys - 1) / keys;
+  return nb == 0 ? 0 : static_cast<long long>(tiles) * p.Hkv * (nb + UNIT_COST);
 }
 
-// The whole CTA: total work, equal stretches (a multiple of WARPS blocks, at
-// least MIN_BLOCKS), and the request in which this CTA's begins.  Two passes
+// The whole CTA: total work, equal stretches (at least MIN_CELLS), and the request in which this CTA's begins.  Two passes
 // over the requests, WARPS * 32 at a time; the second ends at the request found.
-template <int ROWS, int MIN_BLOCKS, int WARPS>
+template <int ROWS, int MIN_CELLS, int UNIT_COST, int WARPS>
 __device__ __forceinline__ void kv4_find_start(const Kv4AttnParams& p, int keys, long long* s_scan,
                                                Kv4Start& out) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int THREADS = WARPS * 32;
   long long mine = 0;
-  for (int r = tid; r < p.R; r += THREADS) mine += kv4_work<ROWS>(p, r, keys);
+  for (int r = tid; r < p.R; r += THREADS) mine += kv4_work<ROWS, UNIT_COST>(p, r, keys);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if (lane == 0) s_scan[warp] = mine;
@@ -217,8 +218,7 @@ __device__ __forceinline__ void kv4_find_start(const Kv4AttnParams& p, int keys,
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) total += s_scan[w];
   long long per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < MIN_BLOCKS) per = MIN_BLOCKS;
-  per = (per + WARPS - 1) / WARPS * WARPS;
+  if (per < MIN_CELLS) per = MIN_CELLS;
   const long long at = per * blockIdx.x;
   if (tid == 0) {
     out.at = at;
@@ -231,7 +231,7 @@ __device__ __forceinline__ void kv4_find_start(const Kv4AttnParams& p, int keys,
   long long base = 0;
   for (int r0 = 0; r0 < p.R; r0 += THREADS) {
     const int r = r0 + tid;
-    const long long w = r < p.R ? kv4_work<ROWS>(p, r, keys) : 0;
+    const long long w = r < p.R ? kv4_work<ROWS, UNIT_COST>(p, r, keys) : 0;
     long long inc = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

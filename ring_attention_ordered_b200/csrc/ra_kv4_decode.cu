@@ -56,10 +56,16 @@
 namespace ra {
 namespace kv4d {
 
-constexpr int WARPS = 8;
+#ifndef KV4_WARPS
+#define KV4_WARPS 8
+#endif
+constexpr int WARPS = KV4_WARPS;
 constexpr int THREADS = WARPS * 32;
 constexpr int STAGES = 4;
-constexpr int MIN_BLOCKS = 32;     // blocks below which a stretch is not cut further
+constexpr int MIN_CELLS = 48;     // cells below which a stretch is not cut further
+// What a unit costs beside its blocks (start, merge, store), in blocks: it
+// takes so many cells of the line before its first block.
+constexpr int UNIT_COST = 16;
 constexpr float P_SHIFT = 8.f;     // p vs = 2^P_SHIFT at the reference
 constexpr float P_LIMIT = 32768.f;
 
@@ -113,8 +119,36 @@ __device__ __forceinline__ void code_pairs(uint32_t x, uint32_t (&p)[4]) {
   p[3] = y & 0x00f000f0u;
 }
 
+// Row `row`, elements 4 d4 .. 4 d4 + 3 of the warps' partials, merged in the
+// warps' order.
 template <int D, int NT>
-__global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
+__device__ __forceinline__ float4 merge_warps(const float* s_merge, const float* s_m,
+                                              const float* s_l, int row, int d4, float& m,
+                                              float& ls) {
+  constexpr int ROWS = 8 * NT;
+  m = -INFINITY;
+  ls = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) m = fmaxf(m, s_m[w * ROWS + row]);
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    const float mw = s_m[w * ROWS + row];
+    if (mw == -INFINITY) continue;
+    const float f = mw == m ? 1.f : ex2_approx(mw - m);
+    const float4 x =
+        *reinterpret_cast<const float4*>(s_merge + (w * ROWS + row) * Smem<D, NT>::RS + 4 * d4);
+    a.x = fmaf(f, x.x, a.x);
+    a.y = fmaf(f, x.y, a.y);
+    a.z = fmaf(f, x.z, a.z);
+    a.w = fmaf(f, x.w, a.w);
+    ls = fmaf(f, s_l[w * ROWS + row], ls);
+  }
+  return a;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
     ra_kv4_decode_kernel(const Kv4AttnParams p) {
   using L = Kv4<D>;
   using S = Smem<D, NT>;
@@ -141,7 +175,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
   }
   kv4_fill_empty<D, THREADS>(p, &g_status);
   // the stretch of this CTA: [start.at, start.end) of the line of blocks
-  kv4_find_start<ROWS, MIN_BLOCKS, WARPS>(p, KV4_BLOCK, s_scan, s_start);
+  kv4_find_start<ROWS, MIN_CELLS, UNIT_COST, WARPS>(p, KV4_BLOCK, s_scan, s_start);
   __syncthreads();
   long long at = s_start.at;
   const long long end = s_start.end;
@@ -155,15 +189,20 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
     const int nb = (q.len + KV4_BLOCK - 1) / KV4_BLOCK;
     const int rows = q.n * p.group;
     const int tiles = (rows + ROWS - 1) / ROWS;
-    if (in_r >= static_cast<long long>(tiles) * p.Hkv * nb) {
+    if (nb == 0 || in_r >= static_cast<long long>(tiles) * p.Hkv * (nb + UNIT_COST)) {
       ++r;
       in_r = 0;
       continue;
     }
-    const int unit = static_cast<int>(in_r / nb);
-    const int b0 = static_cast<int>(in_r - static_cast<long long>(unit) * nb);
-    const int take = static_cast<int>(min(end - at, static_cast<long long>(nb - b0)));
-    const int b1 = b0 + take;
+    const int unit = static_cast<int>(in_r / (nb + UNIT_COST));
+    const int off = static_cast<int>(in_r - static_cast<long long>(unit) * (nb + UNIT_COST));
+    const int cells = static_cast<int>(min(end - at, static_cast<long long>(nb + UNIT_COST - off)));
+    const long long u0 = at - off;
+    const int b0 = max(off - UNIT_COST, 0), b1 = off + cells - UNIT_COST;
+    at += cells;
+    in_r += cells;
+    if (b1 <= b0) continue;
+    const int take = b1 - b0;
     const int h = unit / tiles, row0 = (unit - h * tiles) * ROWS;
 
     // ---- copies: lane i looks up the warp's blocks i, i + 32, ...
@@ -424,32 +463,15 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
     __syncthreads();
 
     const bool whole = b0 == 0 && b1 == nb;
-    // the unit's blocks on the line, and the CTAs whose stretches hold them
-    const long long u0 = at - b0;
-    const int c0 = static_cast<int>(u0 / per_cta);
-    const int c1 = static_cast<int>((u0 + nb - 1) / per_cta);
+    // the CTAs whose stretches hold the unit's blocks
+    const int c0 = static_cast<int>((u0 + UNIT_COST) / per_cta);
+    const int c1 = static_cast<int>((u0 + UNIT_COST + nb - 1) / per_cta);
     float* slot = p.partials + (2ll * blockIdx.x + (static_cast<int>(blockIdx.x) == c0)) * KV4_PIECE_FLOATS;
     const int n_rows = min(ROWS, rows - row0);
     for (int i = tid; i < n_rows * (D / 4); i += THREADS) {
       const int row = i / (D / 4), d4 = i - row * (D / 4);
-      float m = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) m = fmaxf(m, s_m[w * ROWS + row]);
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      float ls = 0.f;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        const float mw = s_m[w * ROWS + row];
-        const float f = mw == -INFINITY ? 0.f : mw == m ? 1.f : ex2_approx(mw - m);
-        const float4 x = *reinterpret_cast<const float4*>(s_merge + (w * ROWS + row) * S::RS + 4 * d4);
-        if (f != 0.f) {
-          a.x = fmaf(f, x.x, a.x);
-          a.y = fmaf(f, x.y, a.y);
-          a.z = fmaf(f, x.z, a.z);
-          a.w = fmaf(f, x.w, a.w);
-          ls = fmaf(f, s_l[w * ROWS + row], ls);
-        }
-      }
+      float m, ls;
+      const float4 a = merge_warps<D, NT>(s_merge, s_m, s_l, row, d4, m, ls);
       if (whole) {
         kv4_store(p, q, h, row0 + row, 4 * d4, D, a, m - P_SHIFT, ls);
       } else {
@@ -471,23 +493,51 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1)
       }
       __syncthreads();
       if (s_last) {
-        for (int i = tid; i < n_rows * (D / 4); i += THREADS) {
-          const int row = i / (D / 4), d4 = i - row * (D / 4);
+        // warp w folds the pieces c0 + w, c0 + w + WARPS, ..., then the warps
+        // are merged as before
+        constexpr int LPR = D / 4;             // lanes of a row
+        constexpr int RPW = 32 / LPR;          // rows a warp folds at once
+        const int d4 = lane % LPR;
+        for (int rb = 0; rb < n_rows; rb += RPW) {
+          const int row = min(rb + lane / LPR, n_rows - 1);
           float m = -INFINITY, ls = 0.f;
           float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int c = c0; c <= c1; ++c) {
-            const float* src = p.partials + (2ll * c + (c == c0)) * KV4_PIECE_FLOATS;
-            kv4_merge(m, ls, a, __ldcg(src + ROWS * D + row), __ldcg(src + ROWS * D + ROWS + row),
-                      __ldcg(reinterpret_cast<const float4*>(src + row * D + 4 * d4)));
+          constexpr int U = 4;
+          for (int c = c0 + warp; c <= c1; c += U * WARPS) {
+            float mm[U], ll[U];
+            float4 aa[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const int cu = c + u * WARPS;
+              const float* src = p.partials + (2ll * cu + (cu == c0)) * KV4_PIECE_FLOATS;
+              mm[u] = -INFINITY;
+              if (cu <= c1) {
+                mm[u] = __ldcg(src + ROWS * D + row);
+                ll[u] = __ldcg(src + ROWS * D + ROWS + row);
+                aa[u] = __ldcg(reinterpret_cast<const float4*>(src + row * D + 4 * d4));
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+              if (mm[u] != -INFINITY) kv4_merge(m, ls, a, mm[u], ll[u], aa[u]);
           }
+          *reinterpret_cast<float4*>(s_merge + (warp * ROWS + row) * S::RS + 4 * d4) = a;
+          if (d4 == 0) {
+            s_m[warp * ROWS + row] = m;
+            s_l[warp * ROWS + row] = ls;
+          }
+        }
+        __syncthreads();
+        for (int i = tid; i < n_rows * (D / 4); i += THREADS) {
+          const int row = i / (D / 4), d4 = i - row * (D / 4);
+          float m, ls;
+          const float4 a = merge_warps<D, NT>(s_merge, s_m, s_l, row, d4, m, ls);
           kv4_store(p, q, h, row0 + row, 4 * d4, D, a, m - P_SHIFT, ls);
         }
       }
     }
     fence_proxy_async();
     __syncthreads();     // the merge buffer is free for copies again
-    at += take;
-    in_r += take;
   }
 }
 
@@ -497,7 +547,7 @@ cudaError_t launch(const Kv4AttnParams& p, int num_sms, int max_ctas, cudaStream
   cudaError_t e = cudaFuncSetAttribute(ra_kv4_decode_kernel<D, NT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
   if (e != cudaSuccess) return e;
-  int grid = num_sms * (NT == 1 ? 2 : 1);
+  int grid = num_sms * ((NT == 1 ? 16 : 8) / WARPS);
   if (max_ctas > 0 && max_ctas < grid) grid = max_ctas;
   if (grid > KV4_MAX_CTAS) grid = KV4_MAX_CTAS;
   ra_kv4_decode_kernel<D, NT><<<grid, THREADS, S::BYTES, stream>>>(p);
