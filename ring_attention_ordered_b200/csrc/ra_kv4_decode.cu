@@ -30,10 +30,10 @@
 // is the M side, 8 query rows (NT tiles of them) the N side, so the padding of
 // a small group costs idle columns, not tensor time.  The transposition of P
 // between the products is one movmatrix per 8 tokens.  Each warp streams
-// blocks of its own through a private ring of shared-memory stages (one bulk
-// copy a block: block i of the warp is refilled as soon as its words are in
-// registers); the warps of a CTA take every 8th block of the CTA's piece and
-// are merged at its end.
+// pairs of blocks through a private ring of shared-memory stages (one bulk
+// copy a block; a stage is refilled as soon as its words are in registers);
+// the warps of a CTA take every 8th pair of the CTA's piece and are merged
+// at its end.
 //
 // Split: the blocks of all (request, head, row tile) units form one line,
 // request-major, and the CTAs take equal stretches of it, so a long request is spread
@@ -46,6 +46,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "ptx_sm100.cuh"
 #include "ra_internal.h"
@@ -61,7 +62,7 @@ namespace kv4d {
 #endif
 constexpr int WARPS = KV4_WARPS;
 constexpr int THREADS = WARPS * 32;
-constexpr int STAGES = 4;
+constexpr int STAGES = 2;          // of two blocks each
 constexpr int MIN_CELLS = 48;     // cells below which a stretch is not cut further
 // What a unit costs beside its blocks (start, merge, store), in blocks: it
 // takes so many cells of the line before its first block.
@@ -73,7 +74,7 @@ __device__ unsigned long long g_status = 0ull;
 
 template <int D, int NT>
 struct Smem {
-  static constexpr int RING = WARPS * STAGES * Kv4<D>::BLOCK_BYTES;
+  static constexpr int RING = WARPS * STAGES * 2 * Kv4<D>::BLOCK_BYTES;
   static constexpr int ROWS = 8 * NT;
   static constexpr int RS = D + 4;                       // row stride of the merge buffer
   static constexpr int MERGE = WARPS * ROWS * RS * 4;
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
   __shared__ long long s_scan[WARPS + 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t ring = smem_u32(smem) + warp * STAGES * L::BLOCK_BYTES;
+  const uint32_t ring = smem_u32(smem) + warp * STAGES * 2 * L::BLOCK_BYTES;
   const uint32_t bars = smem_u32(smem) + S::OFF_BAR + warp * STAGES * 8;
   float* s_merge = reinterpret_cast<float*>(smem);
   float* s_m = reinterpret_cast<float*>(smem + S::OFF_ML);
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
   const long long per_cta = s_start.per_cta;
   int r = s_start.r;
   long long in_r = s_start.in_r;     // blocks of request r before `at`
-  uint32_t it = 0;                   // blocks this warp has taken from its ring
+  uint32_t it = 0;                   // pairs of blocks this warp has taken from its ring
 
   while (at < end) {
     Kv4Req q = kv4_request(p, r);
@@ -205,39 +206,37 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
     const int take = b1 - b0;
     const int h = unit / tiles, row0 = (unit - h * tiles) * ROWS;
 
-    // ---- copies: lane i looks up the warp's blocks i, i + 32, ...
-    const int n_mine = take > warp ? (take - warp + WARPS - 1) / WARPS : 0;
+    // ---- copies: pair i of this warp is blocks b0 + 2 (warp + WARPS i) and the
+    // next; lane 2 j + x looks up block x of pair j (mod 16)
+    const int pairs = (take + 1) >> 1;
+    const int n_mine = pairs > warp ? (pairs - warp + WARPS - 1) / WARPS : 0;
+    const uint32_t it0 = it;
     int ent = -1;
-    auto lookup = [&](int base) {
-      const int blk = b0 + warp + WARPS * (base + lane);
-      ent = blk < b1 ? kv4_block_index(p, r, h, blk, &g_status) : -1;
-    };
-    auto issue = [&](int i) {   // block i of this warp into stage (it0 + i) % STAGES
-      if ((i & 31) == 0) lookup(i);
-      const int e = __shfl_sync(0xffffffffu, ent, i & 31);
-      if (lane == 0) {
-        const uint32_t s = (it + i) % STAGES;
-        if (e >= 0) {
-          mbar_arrive_expect_tx(bars + 8 * s, L::BLOCK_BYTES);
-          bulk_load(ring + s * L::BLOCK_BYTES,
-                    p.cache + static_cast<long long>(e) * L::BLOCK_BYTES, L::BLOCK_BYTES,
-                    bars + 8 * s);
-        } else {
-          mbar_arrive(bars + 8 * s);
-        }
-      }
-      return e;
-    };
-    uint32_t bad = 0;   // stages whose page is out of range
+    uint32_t have = 0;   // bits 2 s, 2 s + 1: the blocks that stage s holds
     int issued = 0;
     auto issue_next = [&] {
-      if (issued < n_mine) {
-        const uint32_t bit = 1u << ((it + issued) % STAGES);
-        bad = issue(issued) >= 0 ? (bad & ~bit) : (bad | bit);
-        ++issued;
+      if (issued >= n_mine) return;
+      if ((issued & 15) == 0) {
+        const int blk = b0 + 2 * (warp + WARPS * (issued + (lane >> 1))) + (lane & 1);
+        ent = blk < b1 ? kv4_block_index(p, r, h, blk, &g_status) : -1;
       }
+      const int e0 = __shfl_sync(0xffffffffu, ent, 2 * (issued & 15));
+      const int e1 = __shfl_sync(0xffffffffu, ent, 2 * (issued & 15) + 1);
+      const uint32_t s = (it0 + issued) % STAGES;
+      have = (have & ~(3u << (2 * s))) | ((e0 >= 0 ? 1u : 0u) << (2 * s)) |
+             ((e1 >= 0 ? 2u : 0u) << (2 * s));
+      if (lane == 0) {
+        const uint32_t bar = bars + 8 * s, dst = ring + s * (2 * L::BLOCK_BYTES);
+        mbar_arrive_expect_tx(bar, L::BLOCK_BYTES * ((e0 >= 0) + (e1 >= 0)));
+        if (e0 >= 0)
+          bulk_load(dst, p.cache + static_cast<long long>(e0) * L::BLOCK_BYTES, L::BLOCK_BYTES, bar);
+        if (e1 >= 0)
+          bulk_load(dst + L::BLOCK_BYTES, p.cache + static_cast<long long>(e1) * L::BLOCK_BYTES,
+                    L::BLOCK_BYTES, bar);
+      }
+      ++issued;
     };
-    const uint32_t it0 = it;
+#pragma unroll
     for (int i = 0; i < STAGES; ++i) issue_next();
 
     // ---- q: operand registers, scale and sum of each row
@@ -304,82 +303,94 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
       }
     }
 
-    bool alive = true;
-    for (int i = 0; i < n_mine; ++i) {
+    // One pair of blocks.  TAIL: some of its tokens are hidden from some row.
+      auto step = [&](auto tail_c, int i) {
+      constexpr bool TAIL = decltype(tail_c)::value;
       const uint32_t s = (it0 + i) % STAGES;
-      if (!wait_warp(bars + 8 * s, ((it0 + i) / STAGES) & 1u, cx, KV4_SITE_COPY)) {
-        alive = false;
-        break;
-      }
-      const bool skip = (bad >> s) & 1u;
-      const uint32_t blk = ring + s * L::BLOCK_BYTES;
-      uint32_t k0[WPL], k1[WPL], v0[WPL], v1[WPL];
-      lds_words(k0, blk + g * L::ROW + t * (4 * WPL));
-      lds_words(k1, blk + (g + 8) * L::ROW + t * (4 * WPL));
-      lds_words(v0, blk + L::OFF_V + lane * (4 * WPL));
-      lds_words(v1, blk + L::OFF_V + 4 * D + lane * (4 * WPL));
-      const uint32_t kp0 = lds32(blk + L::OFF_KP + 4 * g), kp1 = lds32(blk + L::OFF_KP + 4 * g + 32);
-      const uint32_t vp0 = lds32(blk + L::OFF_VP + 4 * g), vp1 = lds32(blk + L::OFF_VP + 4 * g + 32);
-      __syncwarp();
-      issue_next();
-      if (skip) continue;
-
-      float c[NT][4];
+      const uint32_t held = (have >> (2 * s)) & 3u;
+      const uint32_t blk = ring + s * (2 * L::BLOCK_BYTES);
+      float c[NT][2][4];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) c[j][0] = c[j][1] = c[j][2] = c[j][3] = 0.f;
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int w = 0; w < WPL; ++w) {
-        uint32_t a[4], b[4];
-        code_pairs(k0[w], a);
-        code_pairs(k1[w], b);
+        for (int x = 0; x < 2; ++x) c[j][x][0] = c[j][x][1] = c[j][x][2] = c[j][x][3] = 0.f;
+      uint32_t kp[2][2], vp[2][2], v0[2][WPL], v1[2][WPL];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          mma_f16(c[j], a[0], b[0], a[1], b[1], qf[j][2 * w][0], qf[j][2 * w][1]);
-          mma_f16(c[j], a[2], b[2], a[3], b[3], qf[j][2 * w + 1][0], qf[j][2 * w + 1][1]);
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t at = blk + x * L::BLOCK_BYTES;
+        uint32_t k0[WPL], k1[WPL];
+        lds_words(k0, at + g * L::ROW + t * (4 * WPL));
+        lds_words(k1, at + (g + 8) * L::ROW + t * (4 * WPL));
+        kp[x][0] = lds32(at + L::OFF_KP + 4 * g);
+        kp[x][1] = lds32(at + L::OFF_KP + 4 * g + 32);
+        vp[x][0] = lds32(at + L::OFF_VP + 4 * g);
+        vp[x][1] = lds32(at + L::OFF_VP + 4 * g + 32);
+#pragma unroll
+        for (int w = 0; w < WPL; ++w) {
+          uint32_t a[4], b[4];
+          code_pairs(k0[w], a);
+          code_pairs(k1[w], b);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            mma_f16(c[j][x], a[0], b[0], a[1], b[1], qf[j][2 * w][0], qf[j][2 * w][1]);
+            mma_f16(c[j][x], a[2], b[2], a[3], b[3], qf[j][2 * w + 1][0], qf[j][2 * w + 1][1]);
+          }
         }
+        lds_words(v0[x], at + L::OFF_V + lane * (4 * WPL));
+        lds_words(v1[x], at + L::OFF_V + 4 * D + lane * (4 * WPL));
       }
+      __syncwarp();
+      issue_next();   // everything of the stage is in registers
 
-      const float2 ks0 = kv4_params(kp0), ks1 = kv4_params(kp1);
-      const float2 vs0 = kv4_params(vp0), vs1 = kv4_params(vp1);
-      const int key = (b0 + warp + WARPS * i) * KV4_BLOCK + g;
-      const bool tail = (b0 + warp + WARPS * i + 1) * KV4_BLOCK > lim_min;
-      uint32_t pb[NT][2];
+      const int key = (b0 + 2 * (warp + WARPS * i)) * KV4_BLOCK + g;
+      uint32_t pb[NT][2][2];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        // scores without the reference, log2 units
-        float sc[4];
-        sc[0] = fmaf(c[j][0] * rho[j][0], ks0.x, ks0.y * sigma[j][0]);
-        sc[1] = fmaf(c[j][1] * rho[j][1], ks0.x, ks0.y * sigma[j][1]);
-        sc[2] = fmaf(c[j][2] * rho[j][0], ks1.x, ks1.y * sigma[j][0]);
-        sc[3] = fmaf(c[j][3] * rho[j][1], ks1.x, ks1.y * sigma[j][1]);
-        float e[4], pv[4];
+        // element [x][q]: token key + 16 x + 8 (q / 2), query column 2 t + q % 2
+        float e[2][4], pv[2][4];
+        auto hidden = [&](int x, int q4) {
+          return key + 16 * x + 8 * (q4 >> 1) >= lim[j][q4 & 1] || !((held >> x) & 1u);
+        };
         auto weights = [&] {
 #pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {
-            e[q4] = ex2_approx(sc[q4] + mo[j][q4 & 1]);
-            pv[q4] = e[q4] * (q4 < 2 ? vs0.x : vs1.x);
-          }
-          if (tail) {
+          for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4)
-              if (key + (q4 < 2 ? 0 : 8) >= lim[j][q4 & 1]) e[q4] = pv[q4] = 0.f;
+            for (int q4 = 0; q4 < 4; ++q4) {
+              const float2 ks = kv4_params(kp[x][q4 >> 1]);
+              const float2 vs = kv4_params(vp[x][q4 >> 1]);
+              const int cc = q4 & 1;
+              // the score exactly as the reference below is formed from it:
+              // scores may be so large that another rounding is a big factor
+              const float sc = fmaf(c[j][x][q4] * rho[j][cc], ks.x, ks.y * sigma[j][cc]);
+              e[x][q4] = ex2_approx(sc + mo[j][cc]);
+              pv[x][q4] = e[x][q4] * vs.x;
+            }
+          if constexpr (TAIL) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int q4 = 0; q4 < 4; ++q4)
+                if (hidden(x, q4)) e[x][q4] = pv[x][q4] = 0.f;
           }
         };
         weights();
-        const float top = fmaxf(fmaxf(pv[0], pv[1]), fmaxf(pv[2], pv[3]));
-        const bool nan = pv[0] != pv[0] || pv[1] != pv[1] || pv[2] != pv[2] || pv[3] != pv[3];
-        if (__any_sync(0xffffffffu, nan || top > P_LIMIT)) {
+        // the sum bounds each of them, and is NaN if one is
+        const float top = ((pv[0][0] + pv[0][1]) + (pv[0][2] + pv[0][3])) +
+                          ((pv[1][0] + pv[1][1]) + (pv[1][2] + pv[1][3]));
+        if (__any_sync(0xffffffffu, !(top <= P_LIMIT))) {
           // move the reference to the largest s + log2(vs) so far
-          const float lv0 = __log2f(fmaxf(vs0.x, 5.9604645e-8f));
-          const float lv1 = __log2f(fmaxf(vs1.x, 5.9604645e-8f));
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
-            float w0 = sc[cc] + lv0, w1 = sc[2 + cc] + lv1;
-            if (tail) {
-              if (key >= lim[j][cc]) w0 = -INFINITY;
-              if (key + 8 >= lim[j][cc]) w1 = -INFINITY;
-            }
-            float w = fmaxf(w0, w1);
+            float w = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const float2 ks = kv4_params(kp[x][y]);
+                const float lv = __log2f(fmaxf(kv4_params(vp[x][y]).x, 5.9604645e-8f));
+                const float sc = fmaf(c[j][x][2 * y + cc] * rho[j][cc], ks.x, ks.y * sigma[j][cc]);
+                if (!TAIL || !hidden(x, 2 * y + cc)) w = fmaxf(w, sc + lv);
+              }
             w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 4));
             w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 8));
             w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 16));
@@ -396,33 +407,50 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
           }
           weights();
         }
-        l[j][0] += e[0] + e[2];
-        l[j][1] += e[1] + e[3];
-        if (tail) {
-          // a hidden token's parameters may be NaN: 0 times them is not 0
 #pragma unroll
-          for (int cc = 0; cc < 2; ++cc) {
-            if (key < lim[j][cc]) z[j][cc] = fmaf(e[cc], vs0.y, z[j][cc]);
-            if (key + 8 < lim[j][cc]) z[j][cc] = fmaf(e[2 + cc], vs1.y, z[j][cc]);
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+            const float vz = kv4_params(vp[x][q4 >> 1]).y;
+            const int cc = q4 & 1;
+            l[j][cc] += e[x][q4];
+            // a hidden token's zero may be NaN: 0 times it is not 0
+            if (!TAIL || !hidden(x, q4)) z[j][cc] = fmaf(e[x][q4], vz, z[j][cc]);
           }
-        } else {
-          z[j][0] = fmaf(e[0], vs0.y, fmaf(e[2], vs1.y, z[j][0]));
-          z[j][1] = fmaf(e[1], vs0.y, fmaf(e[3], vs1.y, z[j][1]));
-        }
-        pb[j][0] = transpose8(pack_f16x2(pv[0], pv[1]));
-        pb[j][1] = transpose8(pack_f16x2(pv[2], pv[3]));
-      }
-#pragma unroll
-      for (int w = 0; w < WPL; ++w) {
-        uint32_t a[4], b[4];
-        code_pairs(v0[w], a);
-        code_pairs(v1[w], b);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          mma_f16(o[j][2 * w], a[0], a[1], b[0], b[1], pb[j][0], pb[j][1]);
-          mma_f16(o[j][2 * w + 1], a[2], a[3], b[2], b[3], pb[j][0], pb[j][1]);
+          pb[j][x][0] = transpose8(pack_f16x2(pv[x][0], pv[x][1]));
+          pb[j][x][1] = transpose8(pack_f16x2(pv[x][2], pv[x][3]));
         }
       }
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int w = 0; w < WPL; ++w) {
+          uint32_t a[4], b[4];
+          code_pairs(v0[x][w], a);
+          code_pairs(v1[x][w], b);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            mma_f16(o[j][2 * w], a[0], a[1], b[0], b[1], pb[j][x][0], pb[j][x][1]);
+            mma_f16(o[j][2 * w + 1], a[2], a[3], b[2], b[3], pb[j][x][0], pb[j][x][1]);
+          }
+        }
+    };
+    // pairs whose tokens every row sees, as long as their pages are there;
+    // then the others
+    const int n_seen = max(min(lim_min, b1 * KV4_BLOCK) / KV4_BLOCK - b0, 0) >> 1;
+    const int n_full = n_seen > warp ? min((n_seen - warp + WARPS - 1) / WARPS, n_mine) : 0;
+    bool alive = true;
+    int done = 0;
+    for (; done < n_full; ++done) {
+      const uint32_t s = (it0 + done) % STAGES;
+      alive = wait_warp(bars + 8 * s, ((it0 + done) / STAGES) & 1u, cx, KV4_SITE_COPY);
+      if (!alive || ((have >> (2 * s)) & 3u) != 3u) break;
+      step(std::false_type{}, done);
+    }
+    for (; alive && done < n_mine; ++done) {
+      const uint32_t s = (it0 + done) % STAGES;
+      alive = wait_warp(bars + 8 * s, ((it0 + done) / STAGES) & 1u, cx, KV4_SITE_COPY);
+      if (alive) step(std::true_type{}, done);
     }
     if (!alive) {
       // let the copies in flight land before the shared memory goes
