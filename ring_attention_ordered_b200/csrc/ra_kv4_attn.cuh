@@ -185,75 +185,77 @@ __device__ __forceinline__ void kv4_fill_empty(const Kv4AttnParams& p, unsigned 
   }
 }
 
-// Where this CTA's stretch of the line of blocks begins and ends.
-struct Kv4Start {
-  long long at, end, per_cta, in_r;
-  int r;
-};
-
-// Cells that request r takes on the line: for each of its units the blocks of
-// `keys` tokens, and UNIT_COST before them.
+// Cells that request r takes on the line of work: for each of its units
+// (head, row tile) the blocks of its tokens, and UNIT_COST before them.
 template <int ROWS, int UNIT_COST>
-__device__ __forceinline__ long long kv4_work(const Kv4AttnParams& p, int r, int keys) {
+__device__ __forceinline__ long long kv4_work(const Kv4AttnParams& p, int r) {
   const Kv4Req q = kv4_request(p, r);
   const int tiles = (q.n * p.group + ROWS - 1) / ROWS;
-  const int nb = (q.len + keys - 1) / keys;
+  const int nb = (q.len + KV4_BLOCK - 1) / KV4_BLOCK;
   return nb == 0 ? 0 : static_cast<long long>(tiles) * p.Hkv * (nb + UNIT_COST);
 }
 
-// The whole CTA: total work, equal stretches (at least MIN_CELLS), and the request in which this CTA's begins.  Two passes
-// over the requests, WARPS * 32 at a time; the second ends at the request found.
+// Where a warp's stretch of the line begins: cell in_r of request r.
+struct Kv4Start {
+  long long in_r;
+  int r;
+};
+
+// The whole CTA: the line's length, the stretch of one warp (`per` cells, at
+// least MIN_CELLS, the same for every warp of the launch) and the request in
+// which each of this CTA's warps begins.  Requests are taken WARPS * 32 at a
+// time; the second pass ends once the last warp's is found.  Ends with the
+// CTA's threads synchronised.
 template <int ROWS, int MIN_CELLS, int UNIT_COST, int WARPS>
-__device__ __forceinline__ void kv4_find_start(const Kv4AttnParams& p, int keys, long long* s_scan,
-                                               Kv4Start& out) {
+__device__ __forceinline__ void kv4_find_start(const Kv4AttnParams& p, long long* s_scan,
+                                               Kv4Start* out, long long& per, long long& total) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int THREADS = WARPS * 32;
-  long long mine = 0;
-  for (int r = tid; r < p.R; r += THREADS) mine += kv4_work<ROWS, UNIT_COST>(p, r, keys);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) s_scan[warp] = mine;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) total += s_scan[w];
-  long long per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < MIN_CELLS) per = MIN_CELLS;
-  const long long at = per * blockIdx.x;
-  if (tid == 0) {
-    out.at = at;
-    out.end = at >= total ? at : (at + per < total ? at + per : total);
-    out.per_cta = per;
-    out.r = 0;
-    out.in_r = 0;
-  }
-  if (at >= total) return;   // the same in every thread
-  long long base = 0;
-  for (int r0 = 0; r0 < p.R; r0 += THREADS) {
-    const int r = r0 + tid;
-    const long long w = r < p.R ? kv4_work<ROWS, UNIT_COST>(p, r, keys) : 0;
-    long long inc = w;
+  const long long first = tid < p.R ? kv4_work<ROWS, UNIT_COST>(p, tid) : 0;
+  long long mine = first;
+  for (int r = tid + THREADS; r < p.R; r += THREADS) mine += kv4_work<ROWS, UNIT_COST>(p, r);
+  // one scan gives the total, and the places of the first THREADS requests
+  auto scan = [&](long long x, long long& sum) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_scan[warp] = x;
+    __syncthreads();
+    long long before = 0;
+    sum = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) before += s_scan[w];
+      sum += s_scan[w];
     }
     __syncthreads();
-    if (lane == 31) s_scan[warp] = inc;
-    __syncthreads();
-    long long before = base, all = base;
+    return before + x;
+  };
+  long long hi = scan(mine, total);
+  const long long warps = static_cast<long long>(gridDim.x) * WARPS;
+  per = (total + warps - 1) / warps;
+  if (per < MIN_CELLS) per = MIN_CELLS;
+  const long long cta0 = per * (static_cast<long long>(blockIdx.x) * WARPS);
+  long long base = 0;
+  for (int r0 = 0; r0 < p.R && base <= cta0 + (WARPS - 1) * per; r0 += THREADS) {
+    const int r = r0 + tid;
+    long long w = first, all = total;
+    if (p.R > THREADS) {
+      w = r0 == 0 ? first : r < p.R ? kv4_work<ROWS, UNIT_COST>(p, r) : 0;
+      hi = base + scan(w, all);
+      all += base;
+    }
+    const long long lo = hi - w;
+#pragma unroll
     for (int x = 0; x < WARPS; ++x) {
-      if (x < warp) before += s_scan[x];
-      all += s_scan[x];
+      const long long at = cta0 + x * per;
+      if (lo <= at && at < hi) out[x] = {at - lo, r};
     }
-    const long long hi = before + inc, lo = hi - w;
-    if (lo <= at && at < hi) {
-      out.r = r;
-      out.in_r = at - lo;
-    }
-    if (all > at) return;
     base = all;
   }
+  __syncthreads();
 }
 
 }  // namespace ra

@@ -31,16 +31,16 @@
 // a small group costs idle columns, not tensor time.  The transposition of P
 // between the products is one movmatrix per 8 tokens.  Each warp streams
 // pairs of blocks through a private ring of shared-memory stages (one bulk
-// copy a block; a stage is refilled as soon as its words are in registers);
-// the warps of a CTA take every 8th pair of the CTA's piece and are merged
-// at its end.
+// copy a block; a stage is refilled as soon as its words are in registers).
 //
 // Split: the blocks of all (request, head, row tile) units form one line,
-// request-major, and the CTAs take equal stretches of it, so a long request is spread
-// over the GPU and short ones are packed, whatever the lengths, which only
-// the device knows.  A unit that crosses stretches is merged by the CTA that
-// finishes last (a counter that it sets back to zero), over the pieces in
-// their order, so the result does not depend on the order of arrival.
+// request-major, and the warps of the launch take equal stretches of it, so a
+// long request is spread over the GPU and short ones are packed, whatever the
+// lengths, which only the device knows.  A unit inside one warp's stretch is finished by
+// that warp alone, without the CTA; one that crosses warps is merged by their
+// CTA at its end, and one that crosses CTAs by the CTA that finishes last (a
+// counter that it sets back to zero), always over the pieces in their order,
+// so the result does not depend on the order of arrival.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -57,29 +57,42 @@
 namespace ra {
 namespace kv4d {
 
+#ifndef KV4_MINC
+#define KV4_MINC 8
+#endif
+#ifndef KV4_UC
+#define KV4_UC 4
+#endif
+#ifndef KV4_STAGES
+#define KV4_STAGES 2
+#endif
 #ifndef KV4_WARPS
 #define KV4_WARPS 8
 #endif
 constexpr int WARPS = KV4_WARPS;
 constexpr int THREADS = WARPS * 32;
-constexpr int STAGES = 2;          // of two blocks each
-constexpr int MIN_CELLS = 48;     // cells below which a stretch is not cut further
-// What a unit costs beside its blocks (start, merge, store), in blocks: it
+constexpr int STAGES = KV4_STAGES;          // of two blocks each
+constexpr int MIN_CELLS = KV4_MINC;      // cells below which a stretch is not cut further
+// What a unit costs a warp beside its blocks (start, store), in blocks: it
 // takes so many cells of the line before its first block.
-constexpr int UNIT_COST = 16;
+constexpr int UNIT_COST = KV4_UC;
 constexpr float P_SHIFT = 8.f;     // p vs = 2^P_SHIFT at the reference
 constexpr float P_LIMIT = 32768.f;
 
 __device__ unsigned long long g_status = 0ull;
 
+// Shared memory: the warps' rings, a warp's ring taking its tail piece once
+// the warp has read its last block; the head pieces; their m and l; barriers.
 template <int D, int NT>
 struct Smem {
-  static constexpr int RING = WARPS * STAGES * 2 * Kv4<D>::BLOCK_BYTES;
+  static constexpr int WRING = STAGES * 2 * Kv4<D>::BLOCK_BYTES;
   static constexpr int ROWS = 8 * NT;
-  static constexpr int RS = D + 4;                       // row stride of the merge buffer
-  static constexpr int MERGE = WARPS * ROWS * RS * 4;
-  static constexpr int OFF_ML = RING > MERGE ? RING : MERGE;
-  static constexpr int OFF_BAR = OFF_ML + 2 * WARPS * ROWS * 4;
+  static constexpr int RS = D + 4;                       // row stride of a piece
+  static constexpr int PIECE = ROWS * RS * 4;
+  static_assert(PIECE <= WRING, "a piece fits the ring");
+  static constexpr int OFF_HEAD = WARPS * WRING;
+  static constexpr int OFF_ML = OFF_HEAD + WARPS * PIECE;
+  static constexpr int OFF_BAR = OFF_ML + 2 * 2 * WARPS * ROWS * 4;
   static constexpr int BYTES = OFF_BAR + WARPS * STAGES * 8;
 };
 
@@ -120,37 +133,77 @@ __device__ __forceinline__ void code_pairs(uint32_t x, uint32_t (&p)[4]) {
   p[3] = y & 0x00f000f0u;
 }
 
-// Row `row`, elements 4 d4 .. 4 d4 + 3 of the warps' partials, merged in the
-// warps' order.
+// A unit of which this CTA holds pieces: the warps of the launch w0 .. w1.
+struct Group {
+  int r, unit;
+  long long w0, w1;
+};
+
+// The pieces of unit u that CTAs c0 .. c1 left in the workspace, in that order.
+// s_part: shared memory for [parts][items][a, m, l].
 template <int D, int NT>
-__device__ __forceinline__ float4 merge_warps(const float* s_merge, const float* s_m,
-                                              const float* s_l, int row, int d4, float& m,
-                                              float& ls) {
-  constexpr int ROWS = 8 * NT;
-  m = -INFINITY;
-  ls = 0.f;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+__device__ __forceinline__ void kv4_fold(const Kv4AttnParams& p, const Group u, int c0, int c1,
+                                      float* s_part) {
+  constexpr int ROWS = 8 * NT, LPR = D / 4;
+  const int tid = threadIdx.x;
+  const Kv4Req q = kv4_request(p, u.r);
+  const int rows = q.n * p.group, tiles = (rows + ROWS - 1) / ROWS;
+  const int h = u.unit / tiles, row0 = (u.unit - h * tiles) * ROWS;
+  const int n_rows = min(ROWS, rows - row0);
+  // Part y of the threads folds the pieces c0 + y, c0 + y + parts, ... of
+  // (row, 4 elements) x, many loads in flight; the parts are then merged.
+  const int items = n_rows * LPR;
+  const int parts = max(THREADS / items, 1);
+  for (int i = tid; i < items * parts; i += THREADS) {
+    const int y = i / items, x = i - y * items;
+    const int row = x / LPR, d = 4 * (x - row * LPR);
+    float m = -INFINITY, ls = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int U = 8;
+    for (int c = c0 + y; c <= c1; c += U * parts) {
+      float mm[U], ll[U];
+      float4 aa[U];
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) m = fmaxf(m, s_m[w * ROWS + row]);
+      for (int v = 0; v < U; ++v) {
+        const int cv = c + v * parts;
+        const float* src = p.partials + (2ll * cv + (cv == c0)) * KV4_PIECE_FLOATS;
+        mm[v] = -INFINITY;
+        if (cv <= c1) {
+          mm[v] = __ldcg(src + ROWS * D + row);
+          ll[v] = __ldcg(src + ROWS * D + ROWS + row);
+          aa[v] = __ldcg(reinterpret_cast<const float4*>(src + row * D + d));
+        }
+      }
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
-    const float mw = s_m[w * ROWS + row];
-    if (mw == -INFINITY) continue;
-    const float f = mw == m ? 1.f : ex2_approx(mw - m);
-    const float4 x =
-        *reinterpret_cast<const float4*>(s_merge + (w * ROWS + row) * Smem<D, NT>::RS + 4 * d4);
-    a.x = fmaf(f, x.x, a.x);
-    a.y = fmaf(f, x.y, a.y);
-    a.z = fmaf(f, x.z, a.z);
-    a.w = fmaf(f, x.w, a.w);
-    ls = fmaf(f, s_l[w * ROWS + row], ls);
+      for (int v = 0; v < U; ++v)
+        if (mm[v] != -INFINITY) kv4_merge(m, ls, a, mm[v], ll[v], aa[v]);
+    }
+    if (parts == 1) {
+      kv4_store(p, q, h, row0 + row, d, D, a, m - P_SHIFT, ls);
+    } else {
+      float* dst = s_part + 8 * i;
+      *reinterpret_cast<float4*>(dst) = a;
+      dst[4] = m;
+      dst[5] = ls;
+    }
   }
-  return a;
+  if (parts == 1) return;
+  __syncthreads();
+  if (tid < items) {
+    const int row = tid / LPR, d = 4 * (tid - row * LPR);
+    float m = -INFINITY, ls = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int y = 0; y < parts; ++y) {
+      const float* src = s_part + 8 * (y * items + tid);
+      kv4_merge(m, ls, a, src[4], src[5], *reinterpret_cast<const float4*>(src));
+    }
+    kv4_store(p, q, h, row0 + row, d, D, a, m - P_SHIFT, ls);
+  }
 }
 
 template <int D, int NT>
 __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
-    ra_kv4_decode_kernel(const Kv4AttnParams p) {
+    ra_kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p) {
   using L = Kv4<D>;
   using S = Smem<D, NT>;
   constexpr int WPL = D / 32;        // code words of a row per lane (16 or 8 bytes)
@@ -158,35 +211,38 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t s_abort;
   __shared__ int s_last;
-  __shared__ Kv4Start s_start;
-  __shared__ long long s_scan[WARPS + 1];
+  __shared__ Kv4Start s_start[WARPS];
+  __shared__ long long s_scan[WARPS];
+  __shared__ Group s_group[WARPS + 1];   // 0: the CTA's first piece, 1 + w: warp w's tail
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t ring = smem_u32(smem) + warp * STAGES * 2 * L::BLOCK_BYTES;
+  const uint32_t ring = smem_u32(smem) + warp * S::WRING;
   const uint32_t bars = smem_u32(smem) + S::OFF_BAR + warp * STAGES * 8;
-  float* s_merge = reinterpret_cast<float*>(smem);
-  float* s_m = reinterpret_cast<float*>(smem + S::OFF_ML);
-  float* s_l = s_m + WARPS * ROWS;
+  auto piece_at = [&](int w, bool head) {
+    return reinterpret_cast<float*>(smem + (head ? S::OFF_HEAD + w * S::PIECE : w * S::WRING));
+  };
+  float* s_ml = reinterpret_cast<float*>(smem + S::OFF_ML);   // [warp][head][row][m, l]
   const Ctl cx{&s_abort, p.wait_limit_ns, &g_status};
 
   if (tid == 0) s_abort = 0u;
+  if (tid <= WARPS) s_group[tid].r = -1;
   if (lane == 0) {
     for (int i = 0; i < STAGES; ++i) mbar_init(bars + 8 * i, 1);
     fence_mbarrier_init();
   }
-  kv4_fill_empty<D, THREADS>(p, &g_status);
-  // the stretch of this CTA: [start.at, start.end) of the line of blocks
-  kv4_find_start<ROWS, MIN_CELLS, UNIT_COST, WARPS>(p, KV4_BLOCK, s_scan, s_start);
-  __syncthreads();
-  long long at = s_start.at;
-  const long long end = s_start.end;
-  const long long per_cta = s_start.per_cta;
-  int r = s_start.r;
-  long long in_r = s_start.in_r;     // blocks of request r before `at`
+  long long per, total;
+  kv4_find_start<ROWS, MIN_CELLS, UNIT_COST, WARPS>(p, s_scan, s_start, per, total);
+  // the stretch of this warp: [at, end) of the line of cells
+  const long long me = static_cast<long long>(blockIdx.x) * WARPS + warp;
+  long long at = min(me * per, total);
+  const long long end = min(at + per, total);
+  int r = at < end ? s_start[warp].r : 0;
+  long long in_r = at < end ? s_start[warp].in_r : 0;   // cells of request r before `at`
   uint32_t it = 0;                   // pairs of blocks this warp has taken from its ring
+  bool alive = true;
 
   while (at < end) {
-    Kv4Req q = kv4_request(p, r);
+    const Kv4Req q = kv4_request(p, r);
     const int nb = (q.len + KV4_BLOCK - 1) / KV4_BLOCK;
     const int rows = q.n * p.group;
     const int tiles = (rows + ROWS - 1) / ROWS;
@@ -198,7 +254,8 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
     const int unit = static_cast<int>(in_r / (nb + UNIT_COST));
     const int off = static_cast<int>(in_r - static_cast<long long>(unit) * (nb + UNIT_COST));
     const int cells = static_cast<int>(min(end - at, static_cast<long long>(nb + UNIT_COST - off)));
-    const long long u0 = at - off;
+    // the unit's blocks are the cells [first, first + nb)
+    const long long first = at - off + UNIT_COST;
     const int b0 = max(off - UNIT_COST, 0), b1 = off + cells - UNIT_COST;
     at += cells;
     in_r += cells;
@@ -206,10 +263,9 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
     const int take = b1 - b0;
     const int h = unit / tiles, row0 = (unit - h * tiles) * ROWS;
 
-    // ---- copies: pair i of this warp is blocks b0 + 2 (warp + WARPS i) and the
-    // next; lane 2 j + x looks up block x of pair j (mod 16)
-    const int pairs = (take + 1) >> 1;
-    const int n_mine = pairs > warp ? (pairs - warp + WARPS - 1) / WARPS : 0;
+    // ---- copies: pair i is blocks b0 + 2 i and the next; lane j looks up
+    // block j (mod 32) from b0
+    const int n_mine = (take + 1) >> 1;
     const uint32_t it0 = it;
     int ent = -1;
     uint32_t have = 0;   // bits 2 s, 2 s + 1: the blocks that stage s holds
@@ -217,7 +273,7 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
     auto issue_next = [&] {
       if (issued >= n_mine) return;
       if ((issued & 15) == 0) {
-        const int blk = b0 + 2 * (warp + WARPS * (issued + (lane >> 1))) + (lane & 1);
+        const int blk = b0 + 2 * issued + lane;
         ent = blk < b1 ? kv4_block_index(p, r, h, blk, &g_status) : -1;
       }
       const int e0 = __shfl_sync(0xffffffffu, ent, 2 * (issued & 15));
@@ -314,7 +370,7 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int x = 0; x < 2; ++x) c[j][x][0] = c[j][x][1] = c[j][x][2] = c[j][x][3] = 0.f;
-      uint32_t kp[2][2], vp[2][2], v0[2][WPL], v1[2][WPL];
+      uint32_t kp[2][2], vp[2][2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const uint32_t at = blk + x * L::BLOCK_BYTES;
@@ -336,13 +392,9 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
             mma_f16(c[j][x], a[2], b[2], a[3], b[3], qf[j][2 * w + 1][0], qf[j][2 * w + 1][1]);
           }
         }
-        lds_words(v0[x], at + L::OFF_V + lane * (4 * WPL));
-        lds_words(v1[x], at + L::OFF_V + 4 * D + lane * (4 * WPL));
       }
-      __syncwarp();
-      issue_next();   // everything of the stage is in registers
 
-      const int key = (b0 + 2 * (warp + WARPS * i)) * KV4_BLOCK + g;
+      const int key = (b0 + 2 * i) * KV4_BLOCK + g;
       uint32_t pb[NT][2][2];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
@@ -421,6 +473,15 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
           pb[j][x][1] = transpose8(pack_f16x2(pv[x][2], pv[x][3]));
         }
       }
+      uint32_t v0[2][WPL], v1[2][WPL];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t at = blk + x * L::BLOCK_BYTES + L::OFF_V + lane * (4 * WPL);
+        lds_words(v0[x], at);
+        lds_words(v1[x], at + 4 * D);
+      }
+      __syncwarp();
+      issue_next();   // everything of the stage is in registers
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -437,9 +498,7 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
     };
     // pairs whose tokens every row sees, as long as their pages are there;
     // then the others
-    const int n_seen = max(min(lim_min, b1 * KV4_BLOCK) / KV4_BLOCK - b0, 0) >> 1;
-    const int n_full = n_seen > warp ? min((n_seen - warp + WARPS - 1) / WARPS, n_mine) : 0;
-    bool alive = true;
+    const int n_full = max(min(lim_min / KV4_BLOCK, b1) - b0, 0) >> 1;
     int done = 0;
     for (; done < n_full; ++done) {
       const uint32_t s = (it0 + done) % STAGES;
@@ -452,121 +511,131 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
       alive = wait_warp(bars + 8 * s, ((it0 + done) / STAGES) & 1u, cx, KV4_SITE_COPY);
       if (alive) step(std::true_type{}, done);
     }
+    it = it0 + n_mine;
     if (!alive) {
       // let the copies in flight land before the shared memory goes
-      for (int i = 0; i < issued; ++i)
-        if (i + STAGES >= issued && lane == 0)
+      for (int i = max(issued - STAGES, 0); i < issued; ++i)
+        if (lane == 0)
           drain_wait(bars + 8 * ((it0 + i) % STAGES), ((it0 + i) / STAGES) & 1u, 200000000ull);
       __syncwarp();
+      break;
     }
-    it = it0 + n_mine;
 
-    // ---- merge the warps: A = sum p v (relative to m), m, l per row
-    __syncthreads();   // every warp has left its ring, which the buffer overlaps
-    if (s_abort) return;
+    // ---- the piece's result: A = sum p v relative to m, and l
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          l[j][cc] += __shfl_xor_sync(0xffffffffu, l[j][cc], x);
+          z[j][cc] += __shfl_xor_sync(0xffffffffu, z[j][cc], x);
+        }
+    auto values = [&](int j, int cc, int w) {   // elements g d/8 + 4 w .. + 3 of column 2 t + cc
+      return make_float4(fmaf(o[j][2 * w][cc], 16777216.f, z[j][cc]),
+                         fmaf(o[j][2 * w][2 + cc], 1048576.f, z[j][cc]),
+                         fmaf(o[j][2 * w + 1][cc], 16777216.f, z[j][cc]),
+                         fmaf(o[j][2 * w + 1][2 + cc], 1048576.f, z[j][cc]));
+    };
+    const bool head = first < me * per;              // its blocks begin before this warp's
+    const bool open = first + nb > (me + 1) * per;   // and go on behind them
+    if (!head && !open) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          const int row = row0 + 8 * j + 2 * t + cc;
+          if (row < rows)
+#pragma unroll
+            for (int w = 0; w < WPL; ++w)
+              kv4_store(p, q, h, row, g * (D / 8) + 4 * w, D, values(j, cc, w), -mo[j][cc], l[j][cc]);
+        }
+      continue;
+    }
+    if (!head) __syncwarp();   // every lane has read its last block: the ring is free
+    float* dst = piece_at(warp, head);
+    float* ml = s_ml + ((warp * 2 + head) * ROWS) * 2;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
-        float ls = l[j][cc], zs = z[j][cc];
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) {
-          ls += __shfl_xor_sync(0xffffffffu, ls, x);
-          zs += __shfl_xor_sync(0xffffffffu, zs, x);
-        }
         const int row = 8 * j + 2 * t + cc;
-        float* dst = s_merge + (warp * ROWS + row) * S::RS + g * (D / 8);
 #pragma unroll
         for (int w = 0; w < WPL; ++w)
-          *reinterpret_cast<float4*>(dst + 4 * w) =
-              make_float4(fmaf(o[j][2 * w][cc], 16777216.f, zs),
-                          fmaf(o[j][2 * w][2 + cc], 1048576.f, zs),
-                          fmaf(o[j][2 * w + 1][cc], 16777216.f, zs),
-                          fmaf(o[j][2 * w + 1][2 + cc], 1048576.f, zs));
+          *reinterpret_cast<float4*>(dst + row * S::RS + g * (D / 8) + 4 * w) = values(j, cc, w);
         if (g == 0) {
-          s_m[warp * ROWS + row] = P_SHIFT - mo[j][cc];
-          s_l[warp * ROWS + row] = ls;
+          ml[2 * row] = P_SHIFT - mo[j][cc];
+          ml[2 * row + 1] = l[j][cc];
         }
       }
-    __syncthreads();
+    if (lane == 0 && (!head || warp == 0)) 
+      s_group[head ? 0 : 1 + warp] = {r, unit, first / per, (first + nb - 1) / per};
+  }
 
-    const bool whole = b0 == 0 && b1 == nb;
-    // the CTAs whose stretches hold the unit's blocks
-    const int c0 = static_cast<int>((u0 + UNIT_COST) / per_cta);
-    const int c1 = static_cast<int>((u0 + UNIT_COST + nb - 1) / per_cta);
-    float* slot = p.partials + (2ll * blockIdx.x + (static_cast<int>(blockIdx.x) == c0)) * KV4_PIECE_FLOATS;
+  // ---- units that cross warps: merged by the CTA, a row to a warp at a time
+  __syncthreads();
+  if (s_abort) return;
+  const long long cta0 = static_cast<long long>(blockIdx.x) * WARPS;
+  constexpr int LPR = D / 4;             // lanes of a row
+  constexpr int RPW = 32 / LPR;          // rows a warp takes at once
+  const int d4 = 4 * (lane % LPR);
+#pragma unroll 1
+  for (int k = 0; k <= WARPS; ++k) {
+    const Group u = s_group[k];
+    if (u.r < 0) continue;               // the same in every thread
+    const Kv4Req q = kv4_request(p, u.r);
+    const int rows = q.n * p.group, tiles = (rows + ROWS - 1) / ROWS;
+    const int h = u.unit / tiles, row0 = (u.unit - h * tiles) * ROWS;
     const int n_rows = min(ROWS, rows - row0);
-    for (int i = tid; i < n_rows * (D / 4); i += THREADS) {
-      const int row = i / (D / 4), d4 = i - row * (D / 4);
-      float m, ls;
-      const float4 a = merge_warps<D, NT>(s_merge, s_m, s_l, row, d4, m, ls);
-      if (whole) {
-        kv4_store(p, q, h, row0 + row, 4 * d4, D, a, m - P_SHIFT, ls);
+    const int lo = static_cast<int>(max(u.w0, cta0) - cta0);
+    const int hi = static_cast<int>(min(u.w1, cta0 + WARPS - 1) - cta0);
+    const int c0 = static_cast<int>(u.w0 / WARPS), c1 = static_cast<int>(u.w1 / WARPS);
+    float* slot =
+        p.partials + (2ll * blockIdx.x + (static_cast<int>(blockIdx.x) == c0)) * KV4_PIECE_FLOATS;
+    for (int rb = warp * RPW; rb < n_rows; rb += WARPS * RPW) {
+      const int row = rb + lane / LPR;
+      if (row >= n_rows) continue;
+      float m = -INFINITY, ls = 0.f;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        if (w < lo || w > hi) continue;
+        const bool head = cta0 + w != u.w0;
+        const float* ml = s_ml + ((w * 2 + head) * ROWS + row) * 2;
+        kv4_merge(m, ls, a, ml[0], ml[1],
+                  *reinterpret_cast<const float4*>(piece_at(w, head) + row * S::RS + d4));
+      }
+      if (c0 == c1) {
+        kv4_store(p, q, h, row0 + row, d4, D, a, m - P_SHIFT, ls);
       } else {
-        *reinterpret_cast<float4*>(slot + row * D + 4 * d4) = a;
+        *reinterpret_cast<float4*>(slot + row * D + d4) = a;
         if (d4 == 0) {
           slot[ROWS * D + row] = m;
           slot[ROWS * D + ROWS + row] = ls;
         }
       }
     }
-    if (!whole) {
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const unsigned old = atomicAdd(p.counters + c0, 1u);
-        s_last = old == static_cast<unsigned>(c1 - c0);
-        if (s_last) p.counters[c0] = 0u;
-        __threadfence();
-      }
-      __syncthreads();
-      if (s_last) {
-        // warp w folds the pieces c0 + w, c0 + w + WARPS, ..., then the warps
-        // are merged as before
-        constexpr int LPR = D / 4;             // lanes of a row
-        constexpr int RPW = 32 / LPR;          // rows a warp folds at once
-        const int d4 = lane % LPR;
-        for (int rb = 0; rb < n_rows; rb += RPW) {
-          const int row = min(rb + lane / LPR, n_rows - 1);
-          float m = -INFINITY, ls = 0.f;
-          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-          constexpr int U = 4;
-          for (int c = c0 + warp; c <= c1; c += U * WARPS) {
-            float mm[U], ll[U];
-            float4 aa[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-              const int cu = c + u * WARPS;
-              const float* src = p.partials + (2ll * cu + (cu == c0)) * KV4_PIECE_FLOATS;
-              mm[u] = -INFINITY;
-              if (cu <= c1) {
-                mm[u] = __ldcg(src + ROWS * D + row);
-                ll[u] = __ldcg(src + ROWS * D + ROWS + row);
-                aa[u] = __ldcg(reinterpret_cast<const float4*>(src + row * D + 4 * d4));
-              }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-              if (mm[u] != -INFINITY) kv4_merge(m, ls, a, mm[u], ll[u], aa[u]);
-          }
-          *reinterpret_cast<float4*>(s_merge + (warp * ROWS + row) * S::RS + 4 * d4) = a;
-          if (d4 == 0) {
-            s_m[warp * ROWS + row] = m;
-            s_l[warp * ROWS + row] = ls;
-          }
-        }
-        __syncthreads();
-        for (int i = tid; i < n_rows * (D / 4); i += THREADS) {
-          const int row = i / (D / 4), d4 = i - row * (D / 4);
-          float m, ls;
-          const float4 a = merge_warps<D, NT>(s_merge, s_m, s_l, row, d4, m, ls);
-          kv4_store(p, q, h, row0 + row, 4 * d4, D, a, m - P_SHIFT, ls);
-        }
-      }
-    }
-    fence_proxy_async();
-    __syncthreads();     // the merge buffer is free for copies again
   }
+
+  // ---- units that cross CTAs: by the last of them
+  __threadfence();
+  __syncthreads();                       // the pieces in shared memory have been read
+#pragma unroll 1
+  for (int k = 0; k <= WARPS; ++k) {
+    const Group u = s_group[k];
+    const int c0 = static_cast<int>(u.w0 / WARPS), c1 = static_cast<int>(u.w1 / WARPS);
+    if (u.r < 0 || c0 == c1) continue;
+    if (tid == 0) {
+      const unsigned old = atomicAdd(p.counters + c0, 1u);
+      s_last = old == static_cast<unsigned>(c1 - c0);
+      if (s_last) p.counters[c0] = 0u;
+      __threadfence();
+    }
+    __syncthreads();
+    if (s_last) kv4_fold<D, NT>(p, u, c0, c1, reinterpret_cast<float*>(smem));
+    __syncthreads();
+  }
+  kv4_fill_empty<D, THREADS>(p, &g_status);
 }
 
 template <int D, int NT>
