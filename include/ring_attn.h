@@ -439,8 +439,8 @@ ra_status ring_attn_kv4_read(const void* cache, const int32_t* slots, void* k, v
  * ring_attn_kv4_workspace_size -- bytes of device workspace that any call of
  * ring_attn_kv4_fwd needs.  The workspace is zeroed once, before its first
  * call; each call leaves it ready for the next one.  Calls that may run at the same
- * time (streams, replays of captured graphs) need one each.  After
- * RA_ERR_TIMEOUT it has to be zeroed again.
+ * time (streams, replays of captured graphs) need one each.  After an
+ * error from ring_attn_check_status it has to be zeroed again.
  */
 ra_status ring_attn_kv4_workspace_size(size_t* bytes);
 

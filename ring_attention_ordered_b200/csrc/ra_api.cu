@@ -890,7 +890,7 @@ ra_status ring_attn_kv4_fwd(const void* q, int64_t q_stride, const void* cache,
   prm.out_f32 = out_dtype == RA_FP32;
   prm.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   prm.counters = static_cast<unsigned*>(workspace);
-  prm.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + ra::KV4_MAX_CTAS * 4);
+  prm.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + ra::KV4_COUNTER_BYTES);
   prm.wait_limit_ns = g_wait_limit_ns.load();
   const long long rows =
       static_cast<long long>(cu ? (max_q < prm.T ? max_q : prm.T) : 1) * prm.group;

@@ -192,6 +192,8 @@ struct Kv4AttnParams {
   int T, R, Hq, Hkv, group, W, page, num_pages, causal;
   int q_f16, out_f32;
   float scale_log2;       // scale * log2(e)
+  int cell_shift;         // decoding: see Kv4Line
+  int few_units;          // decoding: the units, if they are few, else 0
   unsigned* counters;     // workspace: zero before and after the launch
   float* partials;        // workspace
   unsigned long long wait_limit_ns;
@@ -207,8 +209,9 @@ cudaError_t read_and_clear_kv4_decode_status(unsigned long long* out);
 // into which the launch cuts the work (two a CTA).
 constexpr int KV4_MAX_CTAS = 1024;
 constexpr int KV4_PIECE_FLOATS = 16 * (128 + 2);
+constexpr size_t KV4_COUNTER_BYTES = 3 * KV4_MAX_CTAS * 4;
 constexpr size_t KV4_WORKSPACE_BYTES =
-    KV4_MAX_CTAS * 4 + 2ull * KV4_MAX_CTAS * KV4_PIECE_FLOATS * 4;
+    KV4_COUNTER_BYTES + 2ull * KV4_MAX_CTAS * KV4_PIECE_FLOATS * 4;
 
 cudaError_t launch_round_bf16(const float* src, __nv_bfloat16* dst, long long n, int num_sms,
                               cudaStream_t stream);

@@ -74,36 +74,25 @@ __device__ __forceinline__ int kv4_block_index(const Kv4AttnParams& p, int r, in
   return (id * p.Hkv + h) * bpp + (blk - col * bpp);
 }
 
-// N consecutive elements of packed row `row` of head group h, zeros behind
-// the last row.
+// N consecutive elements of packed row `row` of head group h as they are in
+// memory, zeros behind the last row.
 template <int N>
 __device__ __forceinline__ void kv4_load_q(const Kv4AttnParams& p, const Kv4Req& q, int h, int row,
-                                           int rows, int d0, int d, float (&x)[N]) {
+                                           int rows, int d0, int d, uint4 (&x)[N / 8]) {
   static_assert(N % 8 == 0, "16-byte loads");
-  if (row >= rows) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = 0.f;
-    return;
-  }
+  for (int i = 0; i < N / 8; ++i) x[i] = make_uint4(0, 0, 0, 0);
+  if (row >= rows) return;
   const int tok = row / p.group, head = h * p.group + (row - tok * p.group);
   const uint4* src = reinterpret_cast<const uint4*>(
       static_cast<const uint16_t*>(p.q) + (static_cast<long long>(q.first) + tok) * p.q_stride +
       static_cast<long long>(head) * d + d0);
 #pragma unroll
-  for (int i = 0; i < N / 8; ++i) {
-    const uint4 v = src[i];
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float2 f;
-      if (p.q_f16)
-        f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-      else
-        f = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
-      x[8 * i + 2 * k] = f.x;
-      x[8 * i + 2 * k + 1] = f.y;
-    }
-  }
+  for (int i = 0; i < N / 8; ++i) x[i] = src[i];
+}
+__device__ __forceinline__ float2 kv4_q_pair(const Kv4AttnParams& p, uint32_t w) {
+  return p.q_f16 ? __half22float2(*reinterpret_cast<const __half2*>(&w))
+                 : make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
 // The power of two `up` that brings a row's largest magnitude into [2^14,
@@ -163,7 +152,7 @@ __device__ __forceinline__ void kv4_store(const Kv4AttnParams& p, const Kv4Req& 
 // Dealt over the CTAs by request.  Also the one place that reports numbers
 // outside the tensors.
 template <int D, int THREADS>
-__device__ __forceinline__ void kv4_fill_empty(const Kv4AttnParams& p, unsigned long long* status) {
+__device__ __noinline__ void kv4_fill_empty(const Kv4AttnParams& p, unsigned long long* status) {
   for (int r = blockIdx.x; r < p.R; r += gridDim.x) {
     const Kv4Req q = kv4_request(p, r);
     if (q.bad && threadIdx.x == 0)
@@ -185,77 +174,129 @@ __device__ __forceinline__ void kv4_fill_empty(const Kv4AttnParams& p, unsigned 
   }
 }
 
-// Cells that request r takes on the line of work: for each of its units
-// (head, row tile) the blocks of its tokens, and UNIT_COST before them.
-template <int ROWS, int UNIT_COST>
-__device__ __forceinline__ long long kv4_work(const Kv4AttnParams& p, int r) {
-  const Kv4Req q = kv4_request(p, r);
-  const int tiles = (q.n * p.group + ROWS - 1) / ROWS;
-  const int nb = (q.len + KV4_BLOCK - 1) / KV4_BLOCK;
-  return nb == 0 ? 0 : static_cast<long long>(tiles) * p.Hkv * (nb + UNIT_COST);
-}
-
-// Where a warp's stretch of the line begins: cell in_r of request r.
-struct Kv4Start {
-  long long in_r;
-  int r;
+// The line of work.  Each unit (request, head, row tile) takes cells on it:
+// `lead` cells for what a unit costs beside its blocks, one for each 2^shift
+// blocks, and as many as bring it to a multiple of `align`.  The warps of the
+// launch take equal stretches of `per` cells.
+//
+// Packed (lead > 0, align 1): every warp the same share of the work.  Aligned
+// (lead 0, align a CTA's stretch), for few units: each starts with a CTA, so
+// that a short one is finished in its CTA, and what is left empty behind the
+// units' ends is little beside the whole.
+//
+// Cell numbers are 32 bits wide: the host chooses `shift` so that the longest
+// line the arguments allow stays below 2^31.
+struct Kv4Line {
+  int shift, lead, align, per, total;
+  bool odd;        // some request has no cached token, or numbers that do not fit
+  __device__ __forceinline__ int cells(int nb) const {
+    const int c = ((nb + (1 << shift) - 1) >> shift) + lead;
+    return align == 1 ? c : (c + align - 1) / align * align;
+  }
 };
 
-// The whole CTA: the line's length, the stretch of one warp (`per` cells, at
-// least MIN_CELLS, the same for every warp of the launch) and the request in
-// which each of this CTA's warps begins.  Requests are taken WARPS * 32 at a
-// time; the second pass ends once the last warp's is found.  Ends with the
-// CTA's threads synchronised.
-template <int ROWS, int MIN_CELLS, int UNIT_COST, int WARPS>
-__device__ __forceinline__ void kv4_find_start(const Kv4AttnParams& p, long long* s_scan,
-                                               Kv4Start* out, long long& per, long long& total) {
+// Where a warp's stretch of the line begins: cell `off` of unit `unit` of
+// request r.
+struct Kv4Start {
+  int r, unit, off;
+};
+
+struct Kv4Load {
+  int units, nb;
+  bool odd;
+};
+template <int ROWS>
+__device__ __forceinline__ Kv4Load kv4_load(const Kv4AttnParams& p, int r) {
+  if (r >= p.R) return {0, 0, false};
+  const Kv4Req q = kv4_request(p, r);
+  const int nb = (q.len + KV4_BLOCK - 1) / KV4_BLOCK;
+  return {nb == 0 ? 0 : (q.n * p.group + ROWS - 1) / ROWS * p.Hkv, nb, q.bad || nb == 0};
+}
+
+__device__ __forceinline__ int kv4_warp_scan(int x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// Lays the line out and finds where warp `me` of the launch's `warps` begins.
+// Up to 32 requests each warp does so by itself; more are taken a thread at a
+// time by the CTA (s_scan: WARPS ints, s_start: one a warp).
+template <int ROWS, int WARPS>
+__device__ __forceinline__ Kv4Start kv4_find_start(const Kv4AttnParams& p, int lead, int min_cells,
+                                                   int me, int warps, int* s_scan,
+                                                   Kv4Start* s_start, Kv4Line& line) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int THREADS = WARPS * 32;
-  const long long first = tid < p.R ? kv4_work<ROWS, UNIT_COST>(p, tid) : 0;
-  long long mine = first;
-  for (int r = tid + THREADS; r < p.R; r += THREADS) mine += kv4_work<ROWS, UNIT_COST>(p, r);
-  // one scan gives the total, and the places of the first THREADS requests
-  auto scan = [&](long long x, long long& sum) {
+  line.shift = p.cell_shift;
+  line.lead = lead;
+  line.align = 1;
+  auto stretch = [&] { return max((line.total + warps - 1) / warps, min_cells); };
+  if (p.R <= 32) {
+    const Kv4Load x = kv4_load<ROWS>(p, lane);
+    line.odd = __any_sync(0xffffffffu, x.odd);
+    int all = line.cells(x.nb);
+    int hi = kv4_warp_scan(x.units * all);
+    line.total = __shfl_sync(0xffffffffu, hi, 31);
+    line.per = stretch();
+    if (__reduce_add_sync(0xffffffffu, x.units) <= p.few_units) {
+      // as many stretches as units may be left partly empty
+      const int ctas = warps / WARPS - p.few_units;
+      line.per = max((line.total + ctas * WARPS - 1) / (ctas * WARPS), min_cells);
+      line.lead = 0;
+      line.align = line.per * WARPS;
+      all = line.cells(x.nb);
+      hi = kv4_warp_scan(x.units * all);
+      line.total = __shfl_sync(0xffffffffu, hi, 31);
+    }
+    const int at = me * line.per;
+    const unsigned found = __ballot_sync(0xffffffffu, hi > at);
+    if (found == 0) return {0, 0, 0};
+    const int r = min(__ffs(found) - 1, p.R - 1);
+    const int in = at - (__shfl_sync(0xffffffffu, hi, r) - __shfl_sync(0xffffffffu, x.units * all, r));
+    const int cells = __shfl_sync(0xffffffffu, all, r);
+    const int u = in / cells;
+    return {r, u, in - u * cells};
+  }
+  // thread tid: requests [tid * each, tid * each + each)
+  const int each = (p.R + WARPS * 32 - 1) / (WARPS * 32);
+  int mine = 0;
+  bool odd = false;
+  for (int i = 0; i < each; ++i) {
+    const Kv4Load x = kv4_load<ROWS>(p, tid * each + i);
+    mine += x.units * line.cells(x.nb);
+    odd |= x.odd;
+  }
+  const int inc = kv4_warp_scan(mine);
+  if (lane == 31) s_scan[warp] = inc;
+  line.odd = __syncthreads_or(odd);
+  int lo = inc - mine;
+  line.total = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) lo += s_scan[w];
+    line.total += s_scan[w];
+  }
+  line.per = stretch();
+  // the first of this CTA's warps that begins behind `lo`
+  const int me0 = me - warp;
+  int x = max((lo + line.per - 1) / line.per - me0, 0);
+  if (x < WARPS && (me0 + x) * line.per < lo + mine) {
+    for (int i = 0; i < each; ++i) {
+      const Kv4Load l = kv4_load<ROWS>(p, tid * each + i);
+      const int all = line.cells(l.nb), hi = lo + l.units * all;
+      for (; x < WARPS && (me0 + x) * line.per < hi; ++x) {
+        const int in = (me0 + x) * line.per - lo, u = in / all;
+        s_start[x] = {tid * each + i, u, in - u * all};
+      }
+      lo = hi;
     }
-    if (lane == 31) s_scan[warp] = x;
-    __syncthreads();
-    long long before = 0;
-    sum = 0;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      if (w < warp) before += s_scan[w];
-      sum += s_scan[w];
-    }
-    __syncthreads();
-    return before + x;
-  };
-  long long hi = scan(mine, total);
-  const long long warps = static_cast<long long>(gridDim.x) * WARPS;
-  per = (total + warps - 1) / warps;
-  if (per < MIN_CELLS) per = MIN_CELLS;
-  const long long cta0 = per * (static_cast<long long>(blockIdx.x) * WARPS);
-  long long base = 0;
-  for (int r0 = 0; r0 < p.R && base <= cta0 + (WARPS - 1) * per; r0 += THREADS) {
-    const int r = r0 + tid;
-    long long w = first, all = total;
-    if (p.R > THREADS) {
-      w = r0 == 0 ? first : r < p.R ? kv4_work<ROWS, UNIT_COST>(p, r) : 0;
-      hi = base + scan(w, all);
-      all += base;
-    }
-    const long long lo = hi - w;
-#pragma unroll
-    for (int x = 0; x < WARPS; ++x) {
-      const long long at = cta0 + x * per;
-      if (lo <= at && at < hi) out[x] = {at - lo, r};
-    }
-    base = all;
   }
   __syncthreads();
+  return s_start[warp];
 }
 
 }  // namespace ra

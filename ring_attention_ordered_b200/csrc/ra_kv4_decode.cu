@@ -38,9 +38,10 @@
 // long request is spread over the GPU and short ones are packed, whatever the
 // lengths, which only the device knows.  A unit inside one warp's stretch is finished by
 // that warp alone, without the CTA; one that crosses warps is merged by their
-// CTA at its end, and one that crosses CTAs by the CTA that finishes last (a
-// counter that it sets back to zero), always over the pieces in their order,
-// so the result does not depend on the order of arrival.
+// CTA at its end, and one that crosses CTAs by the CTA that finishes last of
+// each 16, then by the last of these (counters that they set back to zero),
+// always over the pieces in their order, so the result does not depend on the
+// order of arrival.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -76,6 +77,7 @@ constexpr int MIN_CELLS = KV4_MINC;      // cells below which a stretch is not c
 // What a unit costs a warp beside its blocks (start, store), in blocks: it
 // takes so many cells of the line before its first block.
 constexpr int UNIT_COST = KV4_UC;
+constexpr int FOLD = 16;           // pieces that one CTA folds at a time
 constexpr float P_SHIFT = 8.f;     // p vs = 2^P_SHIFT at the reference
 constexpr float P_LIMIT = 32768.f;
 
@@ -135,24 +137,23 @@ __device__ __forceinline__ void code_pairs(uint32_t x, uint32_t (&p)[4]) {
 
 // A unit of which this CTA holds pieces: the warps of the launch w0 .. w1.
 struct Group {
-  int r, unit;
-  long long w0, w1;
+  int r, unit, w0, w1;
 };
 
-// The pieces of unit u that CTAs c0 .. c1 left in the workspace, in that order.
+// Pieces of unit u in the workspace, of the CTAs c0 + i step, i < n, folded in
+// that order: stored as the result, or as the piece of the first of them.
 // s_part: shared memory for [parts][items][a, m, l].
 template <int D, int NT>
-__device__ __forceinline__ void kv4_fold(const Kv4AttnParams& p, const Group u, int c0, int c1,
-                                      float* s_part) {
+__device__ __noinline__ void kv4_fold(const Kv4AttnParams& p, int r, int unit, int c0, int step,
+                                      int n, bool starts, bool finish, float* s_part) {
   constexpr int ROWS = 8 * NT, LPR = D / 4;
   const int tid = threadIdx.x;
-  const Kv4Req q = kv4_request(p, u.r);
+  const Kv4Req q = kv4_request(p, r);
   const int rows = q.n * p.group, tiles = (rows + ROWS - 1) / ROWS;
-  const int h = u.unit / tiles, row0 = (u.unit - h * tiles) * ROWS;
-  const int n_rows = min(ROWS, rows - row0);
-  // Part y of the threads folds the pieces c0 + y, c0 + y + parts, ... of
-  // (row, 4 elements) x, many loads in flight; the parts are then merged.
-  const int items = n_rows * LPR;
+  const int h = unit / tiles, row0 = (unit - h * tiles) * ROWS;
+  const int items = min(ROWS, rows - row0) * LPR;
+  // Part y of the threads folds every parts-th piece of (row, 4 elements) x,
+  // with all loads of a round in flight; then the parts are merged.
   const int parts = max(THREADS / items, 1);
   for (int i = tid; i < items * parts; i += THREADS) {
     const int y = i / items, x = i - y * items;
@@ -160,15 +161,17 @@ __device__ __forceinline__ void kv4_fold(const Kv4AttnParams& p, const Group u, 
     float m = -INFINITY, ls = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int U = 8;
-    for (int c = c0 + y; c <= c1; c += U * parts) {
+#pragma unroll 1
+    for (int c = y; c < n; c += U * parts) {
       float mm[U], ll[U];
       float4 aa[U];
 #pragma unroll
       for (int v = 0; v < U; ++v) {
         const int cv = c + v * parts;
-        const float* src = p.partials + (2ll * cv + (cv == c0)) * KV4_PIECE_FLOATS;
+        const float* src =
+            p.partials + (2ll * (c0 + cv * step) + (starts && cv == 0)) * KV4_PIECE_FLOATS;
         mm[v] = -INFINITY;
-        if (cv <= c1) {
+        if (cv < n) {
           mm[v] = __ldcg(src + ROWS * D + row);
           ll[v] = __ldcg(src + ROWS * D + ROWS + row);
           aa[v] = __ldcg(reinterpret_cast<const float4*>(src + row * D + d));
@@ -178,27 +181,47 @@ __device__ __forceinline__ void kv4_fold(const Kv4AttnParams& p, const Group u, 
       for (int v = 0; v < U; ++v)
         if (mm[v] != -INFINITY) kv4_merge(m, ls, a, mm[v], ll[v], aa[v]);
     }
-    if (parts == 1) {
-      kv4_store(p, q, h, row0 + row, d, D, a, m - P_SHIFT, ls);
-    } else {
-      float* dst = s_part + 8 * i;
-      *reinterpret_cast<float4*>(dst) = a;
-      dst[4] = m;
-      dst[5] = ls;
-    }
+    float* dst = s_part + 8 * i;
+    *reinterpret_cast<float4*>(dst) = a;
+    dst[4] = m;
+    dst[5] = ls;
   }
-  if (parts == 1) return;
-  __syncthreads();
-  if (tid < items) {
-    const int row = tid / LPR, d = 4 * (tid - row * LPR);
+  __syncthreads();   // also: every piece has been read
+  for (int i = tid; i < items; i += THREADS) {
+    const int row = i / LPR, d = 4 * (i - row * LPR);
     float m = -INFINITY, ls = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
     for (int y = 0; y < parts; ++y) {
-      const float* src = s_part + 8 * (y * items + tid);
+      const float* src = s_part + 8 * (y * items + i);
       kv4_merge(m, ls, a, src[4], src[5], *reinterpret_cast<const float4*>(src));
     }
-    kv4_store(p, q, h, row0 + row, d, D, a, m - P_SHIFT, ls);
+    if (finish) {
+      kv4_store(p, q, h, row0 + row, d, D, a, m - P_SHIFT, ls);
+    } else {
+      float* dst = p.partials + (2ll * c0 + starts) * KV4_PIECE_FLOATS;
+      *reinterpret_cast<float4*>(dst + row * D + d) = a;
+      if (d == 0) {
+        dst[ROWS * D + row] = m;
+        dst[ROWS * D + ROWS + row] = ls;
+      }
+    }
   }
+}
+
+// Counts this CTA in at `counter`; true in all of its threads if it is the
+// last of `n`, which sets the counter back to zero.
+__device__ __forceinline__ bool kv4_last(unsigned* counter, int n, int* s_last) {
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const unsigned old = atomicAdd(counter, 1u);
+    *s_last = old == static_cast<unsigned>(n - 1);
+    if (*s_last) *counter = 0u;
+    __threadfence();
+  }
+  __syncthreads();
+  return *s_last != 0;
 }
 
 template <int D, int NT>
@@ -212,7 +235,7 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
   __shared__ uint32_t s_abort;
   __shared__ int s_last;
   __shared__ Kv4Start s_start[WARPS];
-  __shared__ long long s_scan[WARPS];
+  __shared__ int s_scan[WARPS];
   __shared__ Group s_group[WARPS + 1];   // 0: the CTA's first piece, 1 + w: warp w's tail
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -230,38 +253,51 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
     for (int i = 0; i < STAGES; ++i) mbar_init(bars + 8 * i, 1);
     fence_mbarrier_init();
   }
-  long long per, total;
-  kv4_find_start<ROWS, MIN_CELLS, UNIT_COST, WARPS>(p, s_scan, s_start, per, total);
+  __syncthreads();
   // the stretch of this warp: [at, end) of the line of cells
-  const long long me = static_cast<long long>(blockIdx.x) * WARPS + warp;
-  long long at = min(me * per, total);
-  const long long end = min(at + per, total);
-  int r = at < end ? s_start[warp].r : 0;
-  long long in_r = at < end ? s_start[warp].in_r : 0;   // cells of request r before `at`
+  const int me = blockIdx.x * WARPS + warp;
+  Kv4Line line;
+  const Kv4Start start = kv4_find_start<ROWS, WARPS>(p, UNIT_COST, MIN_CELLS, me, gridDim.x * WARPS,
+                                                     s_scan, s_start, line);
+  const int per = line.per;
+  int at = me < (line.total + per - 1) / per ? me * per : line.total;
+  const int end = line.total - at < per ? line.total : at + per;
+  int r = start.r, unit = start.unit, off = start.off;
   uint32_t it = 0;                   // pairs of blocks this warp has taken from its ring
   bool alive = true;
 
-  while (at < end) {
+  while (at < end && r < p.R) {
     const Kv4Req q = kv4_request(p, r);
     const int nb = (q.len + KV4_BLOCK - 1) / KV4_BLOCK;
     const int rows = q.n * p.group;
     const int tiles = (rows + ROWS - 1) / ROWS;
-    if (nb == 0 || in_r >= static_cast<long long>(tiles) * p.Hkv * (nb + UNIT_COST)) {
+    if (nb == 0 || unit >= tiles * p.Hkv) {
       ++r;
-      in_r = 0;
+      unit = off = 0;
       continue;
     }
-    const int unit = static_cast<int>(in_r / (nb + UNIT_COST));
-    const int off = static_cast<int>(in_r - static_cast<long long>(unit) * (nb + UNIT_COST));
-    const int cells = static_cast<int>(min(end - at, static_cast<long long>(nb + UNIT_COST - off)));
-    // the unit's blocks are the cells [first, first + nb)
-    const long long first = at - off + UNIT_COST;
-    const int b0 = max(off - UNIT_COST, 0), b1 = off + cells - UNIT_COST;
+    const int all = line.cells(nb);
+    const int cells = min(end - at, all - off);
+    // the unit's blocks are in the cells [first, last]
+    const int first = at - off + line.lead, last = first + ((nb - 1) >> line.shift);
+    const int b0 = max(off - line.lead, 0) << line.shift;
+    const int b1 = min(max(off + cells - line.lead, 0) << line.shift, nb);
+    const int here = unit;
     at += cells;
-    in_r += cells;
+    off += cells;
+    if (off == all) {
+      ++unit;
+      off = 0;
+    }
     if (b1 <= b0) continue;
     const int take = b1 - b0;
-    const int h = unit / tiles, row0 = (unit - h * tiles) * ROWS;
+    const int h = here / tiles, row0 = (here - h * tiles) * ROWS;
+
+    // ---- q: on its way while the pages are looked up
+    uint4 qw[NT][WPL];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      kv4_load_q<8 * WPL>(p, q, h, row0 + 8 * j + g, rows, t * 8 * WPL, D, qw[j]);
 
     // ---- copies: pair i is blocks b0 + 2 i and the next; lane j looks up
     // block j (mod 32) from b0
@@ -303,7 +339,16 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
     for (int j = 0; j < NT; ++j) {
       const int row = row0 + 8 * j + g;
       float x[8 * WPL];
-      kv4_load_q<8 * WPL>(p, q, h, row, rows, t * 8 * WPL, D, x);
+#pragma unroll
+      for (int i = 0; i < WPL; ++i) {
+        const uint32_t w[4] = {qw[j][i].x, qw[j][i].y, qw[j][i].z, qw[j][i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = kv4_q_pair(p, w[k]);
+          x[8 * i + 2 * k] = f.x;
+          x[8 * i + 2 * k + 1] = f.y;
+        }
+      }
       float am = 0.f, sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 8 * WPL; ++i) {
@@ -538,7 +583,7 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
                          fmaf(o[j][2 * w + 1][2 + cc], 1048576.f, z[j][cc]));
     };
     const bool head = first < me * per;              // its blocks begin before this warp's
-    const bool open = first + nb > (me + 1) * per;   // and go on behind them
+    const bool open = last >= me * per + per;        // and go on behind them
     if (!head && !open) {
 #pragma unroll
       for (int j = 0; j < NT; ++j)
@@ -569,27 +614,29 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
         }
       }
     if (lane == 0 && (!head || warp == 0)) 
-      s_group[head ? 0 : 1 + warp] = {r, unit, first / per, (first + nb - 1) / per};
+      s_group[head ? 0 : 1 + warp] = {r, here, first / per, last / per};
   }
 
   // ---- units that cross warps: merged by the CTA, a row to a warp at a time
   __syncthreads();
   if (s_abort) return;
-  const long long cta0 = static_cast<long long>(blockIdx.x) * WARPS;
+  const int cta0 = blockIdx.x * WARPS;
+  const unsigned groups = __ballot_sync(0xffffffffu, lane <= WARPS && s_group[min(lane, WARPS)].r >= 0);
+  unsigned crossing = 0;                 // groups that other CTAs hold pieces of
   constexpr int LPR = D / 4;             // lanes of a row
   constexpr int RPW = 32 / LPR;          // rows a warp takes at once
   const int d4 = 4 * (lane % LPR);
 #pragma unroll 1
-  for (int k = 0; k <= WARPS; ++k) {
+  for (unsigned rest = groups; rest != 0; rest &= rest - 1) {
+    const int k = __ffs(rest) - 1;
     const Group u = s_group[k];
-    if (u.r < 0) continue;               // the same in every thread
     const Kv4Req q = kv4_request(p, u.r);
     const int rows = q.n * p.group, tiles = (rows + ROWS - 1) / ROWS;
     const int h = u.unit / tiles, row0 = (u.unit - h * tiles) * ROWS;
     const int n_rows = min(ROWS, rows - row0);
-    const int lo = static_cast<int>(max(u.w0, cta0) - cta0);
-    const int hi = static_cast<int>(min(u.w1, cta0 + WARPS - 1) - cta0);
-    const int c0 = static_cast<int>(u.w0 / WARPS), c1 = static_cast<int>(u.w1 / WARPS);
+    const int lo = max(u.w0 - cta0, 0), hi = min(u.w1 - cta0, WARPS - 1);
+    const int c0 = u.w0 / WARPS, c1 = u.w1 / WARPS;
+    if (c0 != c1) crossing |= 1u << k;
     float* slot =
         p.partials + (2ll * blockIdx.x + (static_cast<int>(blockIdx.x) == c0)) * KV4_PIECE_FLOATS;
     for (int rb = warp * RPW; rb < n_rows; rb += WARPS * RPW) {
@@ -597,9 +644,8 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
       if (row >= n_rows) continue;
       float m = -INFINITY, ls = 0.f;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        if (w < lo || w > hi) continue;
+#pragma unroll 1
+      for (int w = lo; w <= hi; ++w) {
         const bool head = cta0 + w != u.w0;
         const float* ml = s_ml + ((w * 2 + head) * ROWS + row) * 2;
         kv4_merge(m, ls, a, ml[0], ml[1],
@@ -617,29 +663,28 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
     }
   }
 
-  // ---- units that cross CTAs: by the last of them
-  __threadfence();
-  __syncthreads();                       // the pieces in shared memory have been read
+  // ---- units that cross CTAs: the last of every FOLD of them folds their
+  // pieces, the last to do so folds these
+  float* s_part = reinterpret_cast<float*>(smem);   // the pieces there have been read
 #pragma unroll 1
-  for (int k = 0; k <= WARPS; ++k) {
-    const Group u = s_group[k];
-    const int c0 = static_cast<int>(u.w0 / WARPS), c1 = static_cast<int>(u.w1 / WARPS);
-    if (u.r < 0 || c0 == c1) continue;
-    if (tid == 0) {
-      const unsigned old = atomicAdd(p.counters + c0, 1u);
-      s_last = old == static_cast<unsigned>(c1 - c0);
-      if (s_last) p.counters[c0] = 0u;
-      __threadfence();
-    }
-    __syncthreads();
-    if (s_last) kv4_fold<D, NT>(p, u, c0, c1, reinterpret_cast<float*>(smem));
-    __syncthreads();
+  for (; crossing != 0; crossing &= crossing - 1) {
+    const Group u = s_group[__ffs(crossing) - 1];
+    const int c0 = u.w0 / WARPS, c1 = u.w1 / WARPS;
+    const int sub = (static_cast<int>(blockIdx.x) - c0) / FOLD, first = c0 + sub * FOLD;
+    const int n = min(FOLD, c1 - first + 1);
+    const bool starts = sub == 0;
+    if (!kv4_last(p.counters + 2 * first + starts, n, &s_last)) continue;
+    const bool one = c1 - c0 < FOLD;
+    kv4_fold<D, NT>(p, u.r, u.unit, first, 1, n, starts, one, s_part);
+    const int subs = (c1 - c0) / FOLD + 1;
+    if (one || !kv4_last(p.counters + 2 * KV4_MAX_CTAS + c0, subs, &s_last)) continue;
+    kv4_fold<D, NT>(p, u.r, u.unit, c0, FOLD, subs, true, true, s_part);
   }
-  kv4_fill_empty<D, THREADS>(p, &g_status);
+  if (line.odd) kv4_fill_empty<D, THREADS>(p, &g_status);
 }
 
 template <int D, int NT>
-cudaError_t launch(const Kv4AttnParams& p, int num_sms, int max_ctas, cudaStream_t stream) {
+cudaError_t launch(Kv4AttnParams p, int num_sms, int max_ctas, cudaStream_t stream) {
   using S = Smem<D, NT>;
   cudaError_t e = cudaFuncSetAttribute(ra_kv4_decode_kernel<D, NT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
@@ -647,6 +692,14 @@ cudaError_t launch(const Kv4AttnParams& p, int num_sms, int max_ctas, cudaStream
   int grid = num_sms * ((NT == 1 ? 16 : 8) / WARPS);
   if (max_ctas > 0 && max_ctas < grid) grid = max_ctas;
   if (grid > KV4_MAX_CTAS) grid = KV4_MAX_CTAS;
+  // units, and with the longest requests the table can name, cells at most;
+  // half a sixteenth of the line is what aligned units leave empty at most
+  const long long tiles = static_cast<long long>(p.T) * p.group / S::ROWS + p.R;
+  const double units = static_cast<double>(tiles) * p.Hkv;
+  p.few_units = p.R <= 32 && units * 16 <= grid ? static_cast<int>(units) : 0;
+  const double blocks = static_cast<double>(p.W) * p.page / KV4_BLOCK;
+  p.cell_shift = 0;
+  while (units * (blocks / (1ll << p.cell_shift) + UNIT_COST + 1) >= 2e9) ++p.cell_shift;
   ra_kv4_decode_kernel<D, NT><<<grid, THREADS, S::BYTES, stream>>>(p);
   return cudaGetLastError();
 }
