@@ -18,7 +18,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libring_attn.so")
 
 SOURCES = ["ra_api.cu", "ra_fwd.cu", "ra_bwd.cu", "ra_merge.cu", "ra_fwd_fp8.cu",
-           "ra_quant_fp8.cu", "ra_kv4_cache.cu", "ra_kv4_decode.cu"]
+           "ra_quant_fp8.cu", "ra_kv4_cache.cu", "ra_kv4_decode.cu",
+           "ra_kv4_chunk.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -32,6 +32,10 @@ std::atomic<unsigned> g_debug_flags{0u};
 std::atomic<int> g_schedule{RA_SCHEDULE_AUTO};
 constexpr double kHeadMajorKvBytes = 96.0 * 1024 * 1024;
 
+// Rows (query tokens times the group's query heads) of a request up to which
+// the decoding kernel serves it.
+constexpr int kKv4DecodeRows = 16;
+
 constexpr int kMaxDevices = 64;
 int g_sm_count[kMaxDevices] = {0};
 int g_cc_ok[kMaxDevices] = {0};  // 0 unknown, 1 yes, -1 no
@@ -889,14 +893,28 @@ ra_status ring_attn_kv4_fwd(const void* q, int64_t q_stride, const void* cache,
   prm.q_f16 = dtype == RA_FP16;
   prm.out_f32 = out_dtype == RA_FP32;
   prm.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  prm.counters = static_cast<unsigned*>(workspace);
-  prm.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + ra::KV4_COUNTER_BYTES);
+  char* ws = static_cast<char*>(workspace);
+  prm.partials = reinterpret_cast<float*>(ws + ra::KV4_COUNTER_BYTES + ra::KV4C_COUNTER_BYTES);
   prm.wait_limit_ns = g_wait_limit_ns.load();
+  // Requests of few rows go to the decoding kernel, those of many to the
+  // chunk kernel; where a batch may hold both, both are launched and each
+  // takes its own.
   const long long rows =
       static_cast<long long>(cu ? (max_q < prm.T ? max_q : prm.T) : 1) * prm.group;
-  cudaError_t e = ra::launch_kv4_decode(prm, d, rows > 1 << 20 ? 1 << 20 : static_cast<int>(rows),
-                                        sms, g_max_ctas.load(),
-                                        reinterpret_cast<cudaStream_t>(stream));
+  const bool chunk = rows > kKv4DecodeRows, decode = !chunk || R > 1;
+  prm.rows_max = chunk ? kKv4DecodeRows : 0x7fffffff;
+  prm.rows_min = decode ? kKv4DecodeRows : 0;
+  cudaError_t e = cudaSuccess;
+  if (decode) {
+    prm.counters = reinterpret_cast<unsigned*>(ws);
+    e = ra::launch_kv4_decode(prm, d, static_cast<int>(rows < kKv4DecodeRows ? rows : kKv4DecodeRows),
+                              sms, g_max_ctas.load(), reinterpret_cast<cudaStream_t>(stream));
+  }
+  if (e == cudaSuccess && chunk) {
+    prm.counters = reinterpret_cast<unsigned*>(ws + ra::KV4_COUNTER_BYTES);
+    e = ra::launch_kv4_chunk(prm, d, sms, g_max_ctas.load(),
+                             reinterpret_cast<cudaStream_t>(stream));
+  }
   if (e != cudaSuccess) return fail(RA_ERR_CUDA, "cache attention launch: %s", cudaGetErrorString(e));
   return ok();
 }
@@ -908,14 +926,16 @@ ra_status ring_attn_check_status(ra_stream_t stream) {
   e = ra::read_and_clear_status(&v);
   if (e == cudaSuccess) e = ra::read_and_clear_bwd_status(&vb);
   if (e == cudaSuccess) e = ra::read_and_clear_fp8_status(&v8);
-  unsigned long long vc = 0, vd = 0;
+  unsigned long long vc = 0, vd = 0, vk = 0;
   if (e == cudaSuccess) e = ra::read_and_clear_kv4_cache_status(&vc);
   if (e == cudaSuccess) e = ra::read_and_clear_kv4_decode_status(&vd);
+  if (e == cudaSuccess) e = ra::read_and_clear_kv4_chunk_status(&vk);
   if (e != cudaSuccess) return fail(RA_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
   if (v == 0) v = vb;
   if (v == 0) v = v8;
   if (v == 0) v = vc;
   if (v == 0) v = vd;
+  if (v == 0) v = vk;
   if (v == 0) return ok();
   const unsigned code = static_cast<unsigned>(v >> 32);
   const unsigned site = static_cast<unsigned>((v >> 16) & 0xFFFF);

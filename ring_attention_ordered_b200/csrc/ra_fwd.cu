@@ -46,6 +46,7 @@
 #include "ra_fwd_roles.cuh"
 #include "ra_internal.h"
 #include "ra_merge_math.cuh"
+#include "ra_mma16.cuh"
 #include "ra_schedule.cuh"
 #include "ra_sync.cuh"
 #include "ring_attn.h"
@@ -55,7 +56,6 @@ namespace ra {
 constexpr int BM = FWD_BM;          // query rows per tile
 constexpr int BN = FWD_BN;          // keys per K/V tile
 constexpr int BOX_COLS = 64;        // TMA box width (64 bf16 = one 128-byte swizzle row)
-constexpr int BOX_BYTES = 128 * 128;
 constexpr int NUM_THREADS = 384;   // three warpgroups
 constexpr int WARP_LOAD = 8;
 constexpr int WARP_MMA = 9;
@@ -102,42 +102,6 @@ struct Cfg {
 };
 
 // ------------------------------------------------------------------ MMA
-template <int KK>
-struct QkStep {
-  static constexpr uint32_t OFF = ((KK / 4) * BOX_BYTES + (KK % 4) * 32) >> 4;
-};
-
-// S = Q K^T over the head dimension: D/16 MMAs of K = 16, each issued by
-// the elected lane.
-template <int D>
-__device__ __forceinline__ void mma_qk_steps(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
-                                             uint32_t idesc) {
-  if (elect_one()) mma_ss<QkStep<0>::OFF, QkStep<0>::OFF>(d, a, hi, b, hi, idesc, 0u);
-  if (elect_one()) mma_ss<QkStep<1>::OFF, QkStep<1>::OFF>(d, a, hi, b, hi, idesc, 1u);
-  if (elect_one()) mma_ss<QkStep<2>::OFF, QkStep<2>::OFF>(d, a, hi, b, hi, idesc, 1u);
-  if (elect_one()) mma_ss<QkStep<3>::OFF, QkStep<3>::OFF>(d, a, hi, b, hi, idesc, 1u);
-  if constexpr (D == 128) {
-    if (elect_one()) mma_ss<QkStep<4>::OFF, QkStep<4>::OFF>(d, a, hi, b, hi, idesc, 1u);
-    if (elect_one()) mma_ss<QkStep<5>::OFF, QkStep<5>::OFF>(d, a, hi, b, hi, idesc, 1u);
-    if (elect_one()) mma_ss<QkStep<6>::OFF, QkStep<6>::OFF>(d, a, hi, b, hi, idesc, 1u);
-    if (elect_one()) mma_ss<QkStep<7>::OFF, QkStep<7>::OFF>(d, a, hi, b, hi, idesc, 1u);
-  }
-}
-
-// O (+)= P V over one half of the 128 keys (HALF 0: keys 0-63, 1: keys
-// 64-127): 4 MMAs of K = 16; P's 16 keys are 8 TMEM columns of bf16 pairs,
-// V's 16 keys are 16 rows of 128 bytes (2048 bytes).  `acc` applies to the
-// first MMA of the first half only.
-template <int HALF>
-__device__ __forceinline__ void mma_pv_half(uint32_t d, uint32_t p_tmem, uint32_t b, uint32_t hi,
-                                            uint32_t idesc, uint32_t acc) {
-  constexpr uint32_t C0 = 32 * HALF, B0 = 512 * HALF;
-  if (elect_one()) mma_ts<C0 + 0, B0 + 0>(d, p_tmem, b, hi, idesc, HALF ? 1u : acc);
-  if (elect_one()) mma_ts<C0 + 8, B0 + 128>(d, p_tmem, b, hi, idesc, 1u);
-  if (elect_one()) mma_ts<C0 + 16, B0 + 256>(d, p_tmem, b, hi, idesc, 1u);
-  if (elect_one()) mma_ts<C0 + 24, B0 + 384>(d, p_tmem, b, hi, idesc, 1u);
-}
-
 // Geometry of the bf16 kernel for the shared loader and MMA roles: a tile
 // row of D bf16 values is D / 64 TMA boxes of 64 columns (one 128-byte
 // swizzle row each), BOX_BYTES apart; tcgen05.mma kind::f16 with K = 16.

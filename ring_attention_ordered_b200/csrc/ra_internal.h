@@ -192,6 +192,10 @@ struct Kv4AttnParams {
   int T, R, Hq, Hkv, group, W, page, num_pages, causal;
   int q_f16, out_f32;
   float scale_log2;       // scale * log2(e)
+  // requests with more rows (query tokens * group) than rows_max are not
+  // the decoding kernel's, those with rows_min or fewer not the chunk kernel's;
+  // rows_min 0: every request is the chunk kernel's
+  int rows_min, rows_max;
   int cell_shift;         // decoding: see Kv4Line
   int few_units;          // decoding: the units, if they are few, else 0
   unsigned* counters;     // workspace: zero before and after the launch
@@ -205,13 +209,21 @@ cudaError_t read_and_clear_kv4_cache_status(unsigned long long* out);
 cudaError_t launch_kv4_decode(const Kv4AttnParams& p, int d, int rows, int num_sms, int max_ctas,
                               cudaStream_t stream);
 cudaError_t read_and_clear_kv4_decode_status(unsigned long long* out);
-// Workspace of kv4 attention: counters, then partial results of the pieces
-// into which the launch cuts the work (two a CTA).
-constexpr int KV4_MAX_CTAS = 1024;
-constexpr int KV4_PIECE_FLOATS = 16 * (128 + 2);
+cudaError_t launch_kv4_chunk(const Kv4AttnParams& p, int d, int num_sms, int max_ctas,
+                             cudaStream_t stream);
+cudaError_t read_and_clear_kv4_chunk_status(unsigned long long* out);
+// Workspace of kv4 attention: the counters of the decoding kernel, those of
+// the chunk kernel (three a CTA each), then partial results of the pieces into
+// which a launch cuts the work (two a CTA; the two kernels, one after the
+// other on the stream, use the same room).
+constexpr int KV4_MAX_CTAS = 1024, KV4C_MAX_CTAS = 160;
+constexpr int KV4_PIECE_FLOATS = 16 * (128 + 2), KV4C_PIECE_FLOATS = 256 * (128 + 2);
 constexpr size_t KV4_COUNTER_BYTES = 3 * KV4_MAX_CTAS * 4;
-constexpr size_t KV4_WORKSPACE_BYTES =
-    KV4_COUNTER_BYTES + 2ull * KV4_MAX_CTAS * KV4_PIECE_FLOATS * 4;
+constexpr size_t KV4C_COUNTER_BYTES = 3 * KV4C_MAX_CTAS * 4;
+constexpr size_t KV4_PARTIAL_BYTES = 2ull * KV4C_MAX_CTAS * KV4C_PIECE_FLOATS * 4;
+static_assert(KV4_PARTIAL_BYTES >= 2ull * KV4_MAX_CTAS * KV4_PIECE_FLOATS * 4, "partials");
+static_assert((KV4_COUNTER_BYTES + KV4C_COUNTER_BYTES) % 16 == 0, "partials are 16-byte aligned");
+constexpr size_t KV4_WORKSPACE_BYTES = KV4_COUNTER_BYTES + KV4C_COUNTER_BYTES + KV4_PARTIAL_BYTES;
 
 cudaError_t launch_round_bf16(const float* src, __nv_bfloat16* dst, long long n, int num_sms,
                               cudaStream_t stream);

@@ -209,8 +209,9 @@ template <int ROWS>
 __device__ __forceinline__ Kv4Load kv4_load(const Kv4AttnParams& p, int r) {
   if (r >= p.R) return {0, 0, false};
   const Kv4Req q = kv4_request(p, r);
-  const int nb = (q.len + KV4_BLOCK - 1) / KV4_BLOCK;
-  return {nb == 0 ? 0 : (q.n * p.group + ROWS - 1) / ROWS * p.Hkv, nb, q.bad || nb == 0};
+  const int nb = (q.len + KV4_BLOCK - 1) / KV4_BLOCK, rows = q.n * p.group;
+  return {nb == 0 || rows > p.rows_max ? 0 : (rows + ROWS - 1) / ROWS * p.Hkv, nb,
+          q.bad || nb == 0};
 }
 
 __device__ __forceinline__ int kv4_warp_scan(int x) {

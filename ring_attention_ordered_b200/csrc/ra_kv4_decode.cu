@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
     const int nb = (q.len + KV4_BLOCK - 1) / KV4_BLOCK;
     const int rows = q.n * p.group;
     const int tiles = (rows + ROWS - 1) / ROWS;
-    if (nb == 0 || unit >= tiles * p.Hkv) {
+    if (nb == 0 || rows > p.rows_max || unit >= tiles * p.Hkv) {
       ++r;
       unit = off = 0;
       continue;

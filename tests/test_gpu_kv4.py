@@ -286,7 +286,12 @@ class Batch:
         * fp32 scores: each of the d + 2 products and sums of a score is off
           by 2^-23 of sum |q| (15 step + |zero|) at most, twice that with the
           exponential's own 2^-22: ds; w ds |v|;
-        * the sums over L keys in fp32, in partial sums: 2^-18 w |v|."""
+        * the sums over L keys in fp32, in partial sums: 2^-18 w |v|.
+        Requests of more than 16 rows (query tokens times the group's heads)
+        go to the chunk kernel, which rounds v and p to fp16 instead of
+        p * step: half a step of each, 2 * 2^-11 w |v|, or 2^-25 of p below
+        fp16's normal range, where the row's largest has 2^5 at least:
+        max |v| 2^-30 a key."""
         at = 0
         half = HALF_STEP[out_dtype or self.dtype]
         out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
@@ -310,8 +315,12 @@ class Batch:
                 ds = 2 * (d + 2) * 2.0 ** -23 * scale * size + 2.0 ** -21
                 ds = np.where(w[:, h] > 0, ds, 0)
                 av = np.abs(v[:, kv].astype(np.float64))
-                tol = (w[:, h] * big[None]).sum(-1)[:, None] * 2.0 ** -11
-                tol = tol + L * big.max() * 2.0 ** -33 + (w[:, h] * (ds + 2.0 ** -18)) @ av
+                if m * (Hq // Hkv) > 16:
+                    tol = 2 * 2.0 ** -11 * (w[:, h] @ av) + L * av.max() * 2.0 ** -30
+                else:
+                    tol = (w[:, h] * big[None]).sum(-1)[:, None] * 2.0 ** -11
+                    tol = tol + L * big.max() * 2.0 ** -33
+                tol = tol + (w[:, h] * (ds + 2.0 ** -18)) @ av
                 tol = tol * (1 + 2 * half) + half * np.abs(ref[:, h]) + 1e-30
                 err = np.abs(got - ref[:, h])
                 assert (err <= tol).all(), (i, h, float((err / tol).max()))
@@ -346,6 +355,11 @@ SHAPES = [
     ([130, 3, 0, 513], [9, 5, 2, 16], 4, 2, 128, 128),  # more query tokens than cached ones
     ([200, 333], [200, 70], 4, 2, 128, 64),             # prompts
     ([391, 1, 129], [131, 1, 129], 3, 1, 64, 16),
+    ([3000], [700], 4, 1, 128, 64),
+    ([257, 1500], [257, 300], 2, 2, 64, 16),
+    ([40, 2100, 0, 300, 128], [300, 64, 5, 1, 128], 8, 2, 128, 32),
+    ([129], [17], 1, 1, 128, 16),
+    ([5000], [3], 8, 1, 64, 128),
 ]
 
 
@@ -412,6 +426,26 @@ def test_attention_of_large_and_small_queries(ra):
     assert (w[0].max(-1) == 1).all()
     err = np.abs(out[0].double().cpu().numpy() - ref[0])
     assert (err <= 2.0 ** -7 * np.abs(ref[0]) + 2.0 ** -9 * np.abs(kv4.kv4_values(*b.kv[0][1])).max()).all()
+
+
+def test_nan_reaches_only_the_rows_that_see_it_in_a_chunk(ra):
+    b = Batch(ra, [300, 40], [200, 30], 2, 1, 128, 16, torch.bfloat16, 7)
+    want = attend(ra, b)
+    k, v = vectors(1, 1, 128, torch.bfloat16, 3)
+    own = b.table[0].tolist()
+    slot = i32([own[177 // 16] * 16 + 177 % 16])
+    old = ra.kv4_read(b.cache, slot)
+    v[0, 0, 3] = math.nan
+    ra.kv4_append(old[0], v.cuda(), slot, b.cache)
+    # query token t of request 0 sees 101 + t tokens: token 177 from t = 77 on
+    out, lse = ra.kv4_fwd(b.q.cuda(), b.cache, b.table, b.len_t, cu=b.cu, max_q=200)
+    assert torch.equal(out[:77], want[0][:77]) and torch.equal(out[200:], want[0][200:])
+    assert torch.isnan(out[77:200]).all() and torch.equal(lse, want[1])
+    k[0, 0, 0] = math.nan
+    ra.kv4_append(k.cuda(), old[1], slot, b.cache)
+    out, lse = ra.kv4_fwd(b.q.cuda(), b.cache, b.table, b.len_t, cu=b.cu, max_q=200)
+    assert torch.equal(out[:77], want[0][:77]) and torch.equal(lse[200:], want[1][200:])
+    assert torch.isnan(out[77:200]).all() and torch.isnan(lse[77:200]).all()
 
 
 def test_nan_reaches_only_the_rows_that_see_it(ra):
