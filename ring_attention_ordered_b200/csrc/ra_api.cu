@@ -34,7 +34,7 @@ constexpr double kHeadMajorKvBytes = 96.0 * 1024 * 1024;
 
 // Rows (query tokens times the group's query heads) of a request up to which
 // the decoding kernel serves it.
-constexpr int kKv4DecodeRows = 16;
+constexpr int kKv4DecodeRows = 128;
 
 constexpr int kMaxDevices = 64;
 int g_sm_count[kMaxDevices] = {0};

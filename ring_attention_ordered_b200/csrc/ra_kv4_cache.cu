@@ -8,6 +8,7 @@
 #include <cstdint>
 
 #include "ra_internal.h"
+#include "ptx_sm100.cuh"
 #include "ra_kv4.cuh"
 
 namespace ra {
@@ -236,6 +237,12 @@ __device__ __forceinline__ uint32_t kv4_code(float x, float zero, float step, fl
 
 // Eight values of one lane; the LANES lanes of the vector agree on its range.
 // Returns the codes (element i in nibble i) and the parameter word.
+//
+// Almost always the codes come from t = (x - zero) * (1 / step) rounded to an
+// integer by adding 1.5 * 2^23, four codes joined as one float below 2^24.  A
+// lane with a value near a border takes kv4_code for its eight, and so does a
+// vector in which t may leave [0, 15]: a step so small that rounding it or the
+// zero to fp16's subnormals counts, or values that were clamped.
 template <class T, int LANES>
 __device__ __forceinline__ uint2 kv4_encode8(uint4 x) {
   using T2 = typename Pair<T>::T2;
@@ -258,17 +265,40 @@ __device__ __forceinline__ uint2 kv4_encode8(uint4 x) {
   if (__half_as_ushort(sh) == 0) sh = __ushort_as_half(1);
   const float zero = __half2float(zh), step = __half2float(sh);
   const float inv = __frcp_rn(step);
-  uint32_t codes = 0;
+  const T2 p[4] = {a, b, c, d};
+  const uint64_t mz2 = f2_pack(-zero, -zero), inv2 = f2_pack(inv, inv);
+  const uint64_t big = f2_pack(12582912.f, 12582912.f), mbig = f2_pack(-12582912.f, -12582912.f);
+  float n[8], off = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 v = Pair<T>::to_float(as_pair<T2>(i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w));
-    codes |= kv4_code(v.x, zero, step, inv) << (8 * i);
-    codes |= kv4_code(v.y, zero, step, inv) << (8 * i + 4);
+    const float2 v = Pair<T>::to_float(p[i]);
+    const uint64_t t = f2_mul(f2_add(f2_pack(v.x, v.y), mz2), inv2);
+    const uint64_t k = f2_add(f2_add(t, big), mbig);
+    float d0, d1;
+    f2_unpack(f2_sub(t, k), d0, d1);
+    f2_unpack(k, n[2 * i], n[2 * i + 1]);
+    off = fmax3(off, fabsf(d0), fabsf(d1));
+  }
+  uint32_t codes = 0;
+  if (off < 0.5f - 1.52587890625e-5f && step >= 1.220703125e-4f && lo == r.x && hi == -r.y) {
+    float q[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      q[h] = fmaf(n[4 * h + 3], 4096.f,
+                  fmaf(n[4 * h + 2], 256.f, fmaf(n[4 * h + 1], 16.f, n[4 * h] + 8388608.f)));
+    codes = __byte_perm(__float_as_uint(q[0]), __float_as_uint(q[1]), 0x5410);
+  } else if (!nan) {
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t w = i < 2 ? x.x : i < 4 ? x.y : i < 6 ? x.z : x.w;
+      const float2 v = Pair<T>::to_float(as_pair<T2>(w));
+      codes |= kv4_code((i & 1) ? v.y : v.x, zero, step, inv) << (4 * i);
+    }
   }
   const uint32_t params = nan ? 0x7FFF7FFFu
                               : static_cast<uint32_t>(__half_as_ushort(sh)) |
                                     (static_cast<uint32_t>(__half_as_ushort(zh)) << 16);
-  return make_uint2(nan ? 0u : codes, params);
+  return make_uint2(codes, params);
 }
 
 // Work items of append and read: one (token, head) to LANES = d / 8 lanes of
@@ -310,6 +340,13 @@ __global__ void __launch_bounds__(CACHE_THREADS) ra_kv4_append_kernel(const Kv4C
   }
   const uint2 kc = kv4_encode8<T, LANES>(k);
   const uint2 vc = kv4_encode8<T, LANES>(v);
+  // neighbouring items are neighbouring tokens of one head; if their slots are
+  // an even one and the next, their V codes share words
+  const int side = it.token & 1;
+  const uint32_t other = __shfl_xor_sync(0xffffffffu, vc.x, LANES);
+  const long long slot2 = __shfl_xor_sync(0xffffffffu, slot, LANES);
+  const bool paired = slot >= 0 && slot2 >= 0 && (slot & 1) == side &&
+                      (side == 0 ? slot2 == slot + 1 : slot2 == slot - 1);
   if (!use) return;
   const long long page = slot / p.page;
   const int o = static_cast<int>(slot - page * p.page);
@@ -317,9 +354,16 @@ __global__ void __launch_bounds__(CACHE_THREADS) ra_kv4_append_kernel(const Kv4C
   uint8_t* blk = p.cache + ((page * p.Hkv + it.head) * (p.page >> 4) + (o >> 4)) * L::BLOCK_BYTES;
   *reinterpret_cast<uint32_t*>(blk + i * L::ROW + j * 4) = kc.x;
   uint8_t* vb = blk + L::OFF_V;
-  *reinterpret_cast<uint16_t*>(vb + L::v_code_offset(i, 2 * j)) = static_cast<uint16_t>(vc.x);
-  *reinterpret_cast<uint16_t*>(vb + L::v_code_offset(i, 2 * j + 1)) =
-      static_cast<uint16_t>(vc.x >> 16);
+  if (paired) {
+    // both tokens of a word in this warp: each lane stores one whole word
+    const uint32_t word = side == 0 ? __byte_perm(vc.x, other, 0x5410)
+                                    : __byte_perm(vc.x, other, 0x3276);
+    *reinterpret_cast<uint32_t*>(vb + L::v_code_offset(i & ~1, 2 * j + side)) = word;
+  } else {
+    *reinterpret_cast<uint16_t*>(vb + L::v_code_offset(i, 2 * j)) = static_cast<uint16_t>(vc.x);
+    *reinterpret_cast<uint16_t*>(vb + L::v_code_offset(i, 2 * j + 1)) =
+        static_cast<uint16_t>(vc.x >> 16);
+  }
   if (j == 0) {
     *reinterpret_cast<uint32_t*>(blk + L::OFF_KP + 4 * i) = kc.y;
     *reinterpret_cast<uint32_t*>(blk + L::OFF_VP + 4 * i) = vc.y;
@@ -345,13 +389,25 @@ __device__ __forceinline__ void store8(__half* dst, const float (&x)[8]) {
   *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// step * code + zero of eight codes.  The nibbles under 0x000f000f are, as
+// fp16 numbers, code 2^-24, under 0x00f000f0 code 2^-20; converted to fp32
+// exactly, the powers of two go into the step, so the one rounding is the
+// sum's, as for the code itself.
 template <class T>
-__device__ __forceinline__ void decode8(T* dst, uint32_t codes, uint32_t params, bool use) {
+__device__ __forceinline__ void decode8(T* dst, uint32_t codes, uint32_t params) {
   const float2 sz = kv4_params(params);
+  const float s24 = sz.x * 16777216.f, s20 = sz.x * 1048576.f;
   float x[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    x[i] = use ? fmaf(sz.x, static_cast<float>((codes >> (4 * i)) & 15u), sz.y) : 0.f;
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w = codes >> (8 * i);
+    const float2 lo = __half22float2(as_pair<__half2>(w & 0x000f000fu));
+    const float2 hi = __half22float2(as_pair<__half2>(w & 0x00f000f0u));
+    x[2 * i] = fmaf(s24, lo.x, sz.y);
+    x[2 * i + 4] = fmaf(s24, lo.y, sz.y);
+    x[2 * i + 1] = fmaf(s20, hi.x, sz.y);
+    x[2 * i + 5] = fmaf(s20, hi.y, sz.y);
+  }
   store8(dst, x);
 }
 
@@ -386,8 +442,8 @@ __global__ void __launch_bounds__(CACHE_THREADS) ra_kv4_read_kernel(const Kv4Cop
     vp = *reinterpret_cast<const uint32_t*>(blk + L::OFF_VP + 4 * i);
   }
   const long long dst = (it.token * p.Hkv + it.head) * D + j * 8;
-  decode8(static_cast<T*>(p.k_out) + dst, kc, kp, use);
-  decode8(static_cast<T*>(p.v_out) + dst, vc, vp, use);
+  decode8(static_cast<T*>(p.k_out) + dst, kc, kp);
+  decode8(static_cast<T*>(p.v_out) + dst, vc, vp);
 }
 
 template <class F>

@@ -54,7 +54,7 @@ constexpr int TILE_ROWS = 128, UNIT_ROWS = 256, TILE_KEYS = 128;
 constexpr int WARP_LOAD = 8, WARP_MMA = 9, WARP_UNPACK = 12;
 // Register split (setmaxnreg) of the launch's 512 x 128.
 constexpr int LAUNCH_REGS = 128;
-constexpr int SOFTMAX_REGS = 192, CONTROL_REGS = 56, UNPACK_REGS = 72;
+constexpr int SOFTMAX_REGS = 200, CONTROL_REGS = 48, UNPACK_REGS = 64;
 static_assert(256 * SOFTMAX_REGS + 128 * CONTROL_REGS + 128 * UNPACK_REGS <= THREADS * LAUNCH_REGS,
               "register split exceeds the launch allocation");
 constexpr int NS = 4;         // operand stages (K or V tile)
@@ -416,7 +416,7 @@ __device__ void unpack_role(const Kv4AttnParams& p, const Bars& br, uint32_t bas
     if (u < 0) break;
     const int n = pieces[u].n_kv, t0 = pieces[u].t0, len = pieces[u].len;
     for (int t = 0; t < n; ++t, ++tile) {
-#pragma unroll
+#pragma unroll 1
       for (int v = 0; v < 2; ++v, ++it) {
         const int rs = it % NRAW, s = it % NS;
         bool ok = wait_bar(br.raw_full(rs), (it / NRAW) & 1u, cx, SITE_RAW_FULL);
@@ -430,7 +430,7 @@ __device__ void unpack_role(const Kv4AttnParams& p, const Bars& br, uint32_t bas
         if (v == 0) {
           // K: 16 bytes are 32 codes of one token, four swizzle chunks
           constexpr int CPR = D / 32;                    // 16-byte chunks of a row
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < CPR; ++c) {
             const int id = i + 128 * c, key = id / CPR, q = id % CPR;
             uint32_t x[4];
@@ -460,7 +460,7 @@ __device__ void unpack_role(const Kv4AttnParams& p, const Bars& br, uint32_t bas
         } else {
           // V: D / 8 bytes of a lane are D / 8 values of two tokens
           constexpr int WPL = D / 32;                    // words of a lane
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             const int id = i + 128 * c;                  // [block][half][lane]
             const int blk = id >> 6, half = (id >> 5) & 1, ln = id & 31;
@@ -571,30 +571,41 @@ __device__ __forceinline__ float weights(uint32_t (&pk)[64], uint32_t tS, uint32
   const uint64_t rho2 = f2_pack(rho, rho), nm2 = f2_pack(nm, nm);
   uint64_t acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
   float mx[2] = {-INFINITY, -INFINITY};
-  uint32_t sr[2][32];
-  tmem_ld32(tS, sr[0]);
+  // two halves of 64 columns in one copy of the code: the tile's loop has to
+  // fit the instruction cache beside the unpacking and MMA loops
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half) {
+    uint32_t sr[2][32];
+    tmem_ld32(tS + 64 * half, sr[0]);
+    if (half == 1) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    tmem_wait_ld();
-    if (c < 3) tmem_ld32(tS + 32 * (c + 1), sr[(c + 1) & 1]);
-    uint32_t(&x)[32] = sr[c & 1];
-    scores32(x, par + 128 * c, sigma2);
+      for (int j = 0; j < 32; ++j) pk[j] = pk[32 + j];
+    }
+    const int left = lim - 64 * half;
+    const uint32_t on = have >> (4 * half);
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      const int col = 32 * c + j;
-      const uint64_t s2 = f2_pack(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
-      float p0, p1;
-      f2_unpack(MASKED ? f2_add(f2_mul(s2, rho2), nm2) : f2_fma(s2, rho2, nm2), p0, p1);
-      if (MASKED) {
-        const bool on = (have >> (col >> 4)) & 1u;
-        if (col > lim || !on) p0 = -INFINITY;
-        if (col + 1 > lim || !on) p1 = -INFINITY;
+    for (int c = 0; c < 2; ++c) {
+      tmem_wait_ld();
+      if (c < 1) tmem_ld32(tS + 64 * half + 32, sr[1]);
+      uint32_t(&x)[32] = sr[c];
+      scores32(x, par + 256 * half + 128 * c, sigma2);
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        const int col = 32 * c + j;
+        const uint64_t s2 = f2_pack(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+        float p0, p1;
+        f2_unpack(MASKED ? f2_add(f2_mul(s2, rho2), nm2) : f2_fma(s2, rho2, nm2), p0, p1);
+        if (MASKED) {
+          const bool in = (on >> (col >> 4)) & 1u;
+          if (col > left || !in) p0 = -INFINITY;
+          if (col + 1 > left || !in) p1 = -INFINITY;
+        }
+        mx[(j >> 1) & 1] = fmax3(mx[(j >> 1) & 1], p0, p1);
+        p0 = ex2_approx(p0);
+        p1 = ex2_approx(p1);
+        acc[(j >> 1) & 1] = f2_add(acc[(j >> 1) & 1], f2_pack(p0, p1));
+        pk[32 + 16 * c + (j >> 1)] = pack_f16x2(p0, p1);
       }
-      mx[(j >> 1) & 1] = fmax3(mx[(j >> 1) & 1], p0, p1);
-      p0 = ex2_approx(p0);
-      p1 = ex2_approx(p1);
-      acc[(j >> 1) & 1] = f2_add(acc[(j >> 1) & 1], f2_pack(p0, p1));
-      pk[16 * c + (j >> 1)] = pack_f16x2(p0, p1);
     }
   }
   float a, b;

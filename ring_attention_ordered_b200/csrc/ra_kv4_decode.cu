@@ -686,9 +686,17 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
 template <int D, int NT>
 cudaError_t launch(Kv4AttnParams p, int num_sms, int max_ctas, cudaStream_t stream) {
   using S = Smem<D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(ra_kv4_decode_kernel<D, NT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
+  static int configured_dev[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured_dev[dev]) {
+    e = cudaFuncSetAttribute(ra_kv4_decode_kernel<D, NT>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
+    if (e != cudaSuccess) return e;
+    configured_dev[dev] = 1;
+  }
   int grid = num_sms * ((NT == 1 ? 16 : 8) / WARPS);
   if (max_ctas > 0 && max_ctas < grid) grid = max_ctas;
   if (grid > KV4_MAX_CTAS) grid = KV4_MAX_CTAS;

@@ -287,7 +287,7 @@ class Batch:
           by 2^-23 of sum |q| (15 step + |zero|) at most, twice that with the
           exponential's own 2^-22: ds; w ds |v|;
         * the sums over L keys in fp32, in partial sums: 2^-18 w |v|.
-        Requests of more than 16 rows (query tokens times the group's heads)
+        Requests of more than 128 rows (query tokens times the group's heads)
         go to the chunk kernel, which rounds v and p to fp16 instead of
         p * step: half a step of each, 2 * 2^-11 w |v|, or 2^-25 of p below
         fp16's normal range, where the row's largest has 2^5 at least:
@@ -315,7 +315,7 @@ class Batch:
                 ds = 2 * (d + 2) * 2.0 ** -23 * scale * size + 2.0 ** -21
                 ds = np.where(w[:, h] > 0, ds, 0)
                 av = np.abs(v[:, kv].astype(np.float64))
-                if m * (Hq // Hkv) > 16:
+                if m * (Hq // Hkv) > 128:
                     tol = 2 * 2.0 ** -11 * (w[:, h] @ av) + L * av.max() * 2.0 ** -30
                 else:
                     tol = (w[:, h] * big[None]).sum(-1)[:, None] * 2.0 ** -11
