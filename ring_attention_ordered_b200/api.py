@@ -310,6 +310,12 @@ _CODE = {torch.bfloat16: _lib.RA_BF16, torch.float16: _lib.RA_FP16, torch.float3
 _workspace_bytes = None
 
 
+# The current stream's handle without building a torch.cuda.Stream, which
+# costs more than the rest of a small call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _Here:
     """``_on`` where nothing has to be switched: the tensors' device is the
     current one and the call uses its current stream."""
@@ -327,9 +333,17 @@ class _Here:
 
 
 def _here(device, stream):
-    if stream is None and torch.cuda.current_device() == device.index:
-        return _Here(torch.cuda.current_stream(device).cuda_stream)
+    index = device.index
+    if stream is None and torch.cuda.current_device() == index:
+        return _Here(_raw_stream(index))
     return _on(device, stream)
+
+
+def _is(t, dtype, ndim: int, device) -> bool:
+    """Whether t is a contiguous tensor of that type and rank on `device`
+    (one expression: these calls are counted in microseconds)."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim
+            and t.device == device and t.is_contiguous())
 
 
 def _check_same_device(device, **tensors):
@@ -403,8 +417,13 @@ def kv4_plan(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, pool: t
     that do not fit), in which case nothing changes.  ``out``: tensors of
     these shapes for the results; the first three may be the inputs
     themselves."""
-    for t, n, k in ((lens, "lens", 1), (add, "add", 1), (table, "table", 2), (pool, "pool", 1)):
-        _check_cuda(t, n, torch.int32, k)
+    i32 = torch.int32
+    _check_cuda(table, "table", i32, 2)
+    dev = table.device
+    if not (_is(lens, i32, 1, dev) and _is(add, i32, 1, dev) and _is(pool, i32, 1, dev)):
+        for t, n in ((lens, "lens"), (add, "add"), (pool, "pool")):
+            _check_cuda(t, n, i32, 1)
+        _check_same_device(dev, lens=lens, add=add, pool=pool)
     R, W = table.shape
     if lens.shape[0] != R or add.shape[0] != R:
         raise ValueError(f"lens {tuple(lens.shape)}, add {tuple(add.shape)} and table "
@@ -412,14 +431,15 @@ def kv4_plan(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, pool: t
     num_pages = pool.shape[0] - 1
     if num_pages < 0:
         raise ValueError("pool must be [num_pages + 1]")
-    dev = table.device
-    _check_same_device(dev, lens=lens, add=add, pool=pool)
+    if max_tokens < 0:
+        raise ValueError(f"max_tokens must be >= 0, got {max_tokens}")
     with _here(dev, stream) as sh:
         if out is None:
-            out = (torch.empty_like(lens), torch.empty_like(table), torch.empty_like(pool),
-                   torch.empty(R + 1, dtype=torch.int32, device=dev),
-                   torch.empty(max_tokens, dtype=torch.int32, device=dev),
-                   torch.empty(1, dtype=torch.int32, device=dev))
+            # one allocation, each part on a 16-byte boundary
+            sizes = [-(-n // 4) * 4 for n in (R * W, num_pages + 1, max_tokens, R, R + 1, 1)]
+            b = torch.empty(sum(sizes), dtype=i32, device=dev).split(sizes)
+            out = (b[3][:R], b[0][:R * W].view(R, W), b[1][:num_pages + 1], b[4][:R + 1],
+                   b[2][:max_tokens], b[5][:1])
         else:
             for t, n, shape in zip(out, ("lens", "table", "pool", "cu", "slots", "shortage"),
                                    ((R,), (R, W), (num_pages + 1,), (R + 1,), (max_tokens,), (1,)),
@@ -444,9 +464,12 @@ def kv4_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: tor
     if k.shape != (T, Hkv, d) or v.shape != k.shape or k.dtype != v.dtype:
         raise ValueError(f"k {tuple(k.shape)} {k.dtype} and v {tuple(v.shape)} {v.dtype} must be "
                          f"[T, {Hkv}, {d}] of one type")
-    _check_out(slots, "slots", torch.int32, (T,))
-    _check_same_device(cache.device, k=k, v=v, slots=slots)
-    with _here(cache.device, stream) as sh:
+    dev = cache.device
+    if not (_is(slots, torch.int32, 1, dev) and slots.shape[0] == T and k.device == dev
+            and v.device == dev):
+        _check_out(slots, "slots", torch.int32, (T,))
+        _check_same_device(dev, k=k, v=v, slots=slots)
+    with _here(dev, stream) as sh:
         _lib.ring_attn_kv4_append(k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(),
                                   cache.data_ptr(), T, Hkv, d, _CODE[k.dtype], P, page, sh)
     return cache
@@ -457,17 +480,24 @@ def kv4_read(cache: torch.Tensor, slots: torch.Tensor, dtype: torch.dtype = torc
     """The cached keys and values at ``slots`` (int32 [T]; zeros for -1):
     (k, v) of ``dtype`` (bf16, fp16 or fp32), [T, Hkv, d]."""
     P, Hkv, page, d = _cache_shape(cache)
-    _check_cuda(slots, "slots", torch.int32, 1)
+    dev = cache.device
+    if not _is(slots, torch.int32, 1, dev):
+        _check_cuda(slots, "slots", torch.int32, 1)
+        _check_same_device(dev, slots=slots)
     if dtype not in _CODE:
         raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
     T = slots.shape[0]
-    dev = cache.device
-    _check_same_device(dev, slots=slots, k=k, v=v)
     with _here(dev, stream) as sh:
-        k = torch.empty((T, Hkv, d), dtype=dtype, device=dev) if k is None else k
-        v = torch.empty((T, Hkv, d), dtype=dtype, device=dev) if v is None else v
-        _check_out(k, "k", dtype, (T, Hkv, d))
-        _check_out(v, "v", dtype, (T, Hkv, d))
+        if k is None:
+            k = torch.empty((T, Hkv, d), dtype=dtype, device=dev)
+        elif not (_is(k, dtype, 3, dev) and k.shape == (T, Hkv, d)):
+            _check_out(k, "k", dtype, (T, Hkv, d))
+            _check_same_device(dev, k=k)
+        if v is None:
+            v = torch.empty((T, Hkv, d), dtype=dtype, device=dev)
+        elif not (_is(v, dtype, 3, dev) and v.shape == (T, Hkv, d)):
+            _check_out(v, "v", dtype, (T, Hkv, d))
+            _check_same_device(dev, v=v)
         _lib.ring_attn_kv4_read(cache.data_ptr(), slots.data_ptr(), k.data_ptr(), v.data_ptr(), T,
                                 Hkv, d, _CODE[dtype], P, page, sh)
     return k, v
@@ -501,37 +531,43 @@ def kv4_fwd(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens: tor
     T, Hq, dq = q.shape
     if dq != d or Hq % Hkv != 0 or Hq < 1:
         raise ValueError(f"q {tuple(q.shape)} does not match a cache of {Hkv} heads of {d}")
-    _check_cuda(table, "table", torch.int32, 2)
+    i32, dev = torch.int32, q.device
+    if not (_is(table, i32, 2, dev) and _is(lens, i32, 1, dev) and cache.device == dev):
+        _check_cuda(table, "table", i32, 2)
+        _check_cuda(lens, "lens", i32, 1)
+        _check_same_device(dev, cache=cache, table=table, lens=lens)
     R, W = table.shape
-    _check_out(lens, "lens", torch.int32, (R,))
+    if lens.shape[0] != R:
+        raise ValueError(f"lens {tuple(lens.shape)} does not match table {tuple(table.shape)}")
     if cu is not None:
-        _check_out(cu, "cu", torch.int32, (R + 1,))
+        if not (_is(cu, i32, 1, dev) and cu.shape[0] == R + 1):
+            _check_out(cu, "cu", i32, (R + 1,))
+            _check_same_device(dev, cu=cu)
     elif T != R:
         raise ValueError(f"without cu every request has one query token, got {T} for {R} requests")
     if max_q is None:
         max_q = T
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    dev = q.device
-    _check_same_device(dev, cache=cache, table=table, lens=lens, cu=cu, out=out, lse=lse,
-                       workspace=workspace)
     if out_dtype is None:
         out_dtype = q.dtype if out is None else out.dtype
-    if out_dtype != q.dtype and out_dtype != torch.float32:
+    if out_dtype is not q.dtype and out_dtype is not torch.float32:
         raise TypeError(f"the output is {q.dtype} or float32, got {out_dtype}")
     with _here(dev, stream) as sh:
         if out is None:
             out = torch.empty((T, Hq, d), dtype=out_dtype, device=dev)
-        else:
+        elif not (_is(out, out_dtype, 3, dev) and out.shape == (T, Hq, d)):
             _check_out(out, "out", out_dtype, (T, Hq, d))
+            _check_same_device(dev, out=out)
         if lse is None:
             lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-        else:
+        elif not (_is(lse, torch.float32, 2, dev) and lse.shape == (T, Hq)):
             _check_out(lse, "lse", torch.float32, (T, Hq))
+            _check_same_device(dev, lse=lse)
         if workspace is None:
             workspace = kv4_workspace(dev)
-        elif not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous CUDA tensor")
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
         _lib.ring_attn_kv4_fwd(q.data_ptr(), qs, cache.data_ptr(), table.data_ptr(),
                                lens.data_ptr(), 0 if cu is None else cu.data_ptr(), out.data_ptr(),
                                lse.data_ptr(), T, R, Hq, Hkv, d, W, P, page, max_q, causal, scale,

@@ -29,7 +29,7 @@ __device__ unsigned long long g_kv4_cache_status = 0ull;
 // are taken again, the table is complete before the slots read it.  The
 // stack positions follow from the prefix sums alone, so the result does not
 // depend on which thread does what.
-constexpr int PLAN_THREADS = 512;
+constexpr int PLAN_THREADS = 1024;
 
 struct PlanSums {
   long long tok;   // new tokens
@@ -53,6 +53,31 @@ __device__ __forceinline__ int find_request(const int* pre, int n, int i) {
     if (pre[mid] <= i) lo = mid; else hi = mid - 1;
   }
   return lo;
+}
+
+// n ints by threads tid, tid + size, ...: 16 bytes at a time where both
+// pointers allow, four loads under way.
+__device__ __forceinline__ void copy_ints(int32_t* dst, const int32_t* src, long long n, int tid,
+                                          int size) {
+  constexpr int U = 4;
+  long long done = 0;
+  if (((reinterpret_cast<uintptr_t>(dst) | reinterpret_cast<uintptr_t>(src)) & 15u) == 0) {
+    const long long n4 = n >> 2;
+    for (long long i = tid; i < n4; i += U * static_cast<long long>(size)) {
+      int4 x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i + u * static_cast<long long>(size) < n4)
+          x[u] = reinterpret_cast<const int4*>(src)[i + u * static_cast<long long>(size)];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i + u * static_cast<long long>(size) < n4)
+          reinterpret_cast<int4*>(dst)[i + u * static_cast<long long>(size)] = x[u];
+    }
+    done = n4 << 2;
+  }
+#pragma unroll 4
+  for (long long i = done + tid; i < n; i += size) dst[i] = src[i];
 }
 
 __global__ void __launch_bounds__(PLAN_THREADS) ra_kv4_plan_kernel(const Kv4PlanParams p) {
@@ -135,13 +160,9 @@ __global__ void __launch_bounds__(PLAN_THREADS) ra_kv4_plan_kernel(const Kv4Plan
 
   cluster.sync();   // every CTA has read lens, add and pool[0]
 
-  if (p.table_out != p.table)
-    for (long long i = gtid; i < static_cast<long long>(R) * p.W; i += gsize)
-      p.table_out[i] = p.table[i];
-  if (p.pool_out != p.pool) {
-    const int n_copy = keep ? p.num_pages : min(left, n_free);
-    for (int i = 1 + gtid; i <= n_copy; i += gsize) p.pool_out[i] = p.pool[i];
-  }
+  if (p.table_out != p.table) copy_ints(p.table_out, p.table, static_cast<long long>(R) * p.W, gtid, gsize);
+  if (p.pool_out != p.pool)
+    copy_ints(p.pool_out + 1, p.pool + 1, keep ? p.num_pages : min(left, n_free), gtid, gsize);
   if (!keep) {
     // above the stack's new top nothing is left
     for (int i = itop + 1 + gtid; i <= p.num_pages; i += gsize) p.pool_out[i] = -1;
@@ -301,72 +322,95 @@ __device__ __forceinline__ uint2 kv4_encode8(uint4 x) {
   return make_uint2(codes, params);
 }
 
-// Work items of append and read: one (token, head) to LANES = d / 8 lanes of
-// 8 elements.  Items run over the tokens of a group of 16 first, then over
-// the heads, so that the two tokens whose V codes share a sector are handled
-// by neighbouring lanes.
+// Work of append and read: LANES = d / 8 lanes take the d values of a token
+// and head, 8 each; a CTA takes 16 tokens (so that the tokens whose V codes
+// share a sector are handled together) of HEADS heads, HEADS * 16 * LANES /
+// CACHE_THREADS of them one after the other in each thread with their loads
+// under way at once.
 constexpr int CACHE_THREADS = 256;
-
-struct Item {
-  long long token;
-  int head;
+constexpr int HEADS_AT_ONCE = 2;      // vectors in flight in a thread
+template <int D>
+struct CacheCta {
+  static constexpr int LANES = D / 8;
+  static constexpr int ACROSS = CACHE_THREADS / (16 * LANES);   // heads side by side
+  static constexpr int HEADS = ACROSS * HEADS_AT_ONCE;
 };
-__device__ __forceinline__ Item item_of(long long i, int Hkv) {
-  const long long group = i / (16 * Hkv);
-  const int rest = static_cast<int>(i - group * (16 * Hkv));
-  return {group * 16 + (rest & 15), rest >> 4};
+struct Place {
+  long long token;
+  int head0, lane;      // head u of the thread: head0 + u * ACROSS
+};
+template <int D>
+__device__ __forceinline__ Place place_of(int Hkv) {
+  using C = CacheCta<D>;
+  const unsigned per = (Hkv + C::HEADS - 1) / C::HEADS;
+  const unsigned group = blockIdx.x / per;
+  const int t = threadIdx.x;
+  return {static_cast<long long>(group) * 16 + (t / C::LANES) % 16,
+          static_cast<int>(blockIdx.x - group * per) * C::HEADS + t / (16 * C::LANES),
+          t % C::LANES};
+}
+// The slot of a token, -1 if it has none (one out of range is reported).
+__device__ __forceinline__ int slot_of(const Kv4CopyParams& p, long long token) {
+  const int slot = token < p.T ? p.slots[token] : -1;
+  if (slot < -1 || slot >= p.num_slots) {
+    kv4_record(&g_kv4_cache_status, RA_ERR_INVALID_ARG, KV4_SITE_SLOT);
+    return -1;
+  }
+  return slot;
 }
 
 template <int D, class T>
 __global__ void __launch_bounds__(CACHE_THREADS) ra_kv4_append_kernel(const Kv4CopyParams p) {
   using L = Kv4<D>;
-  constexpr int LANES = D / 8;
-  const long long tid = static_cast<long long>(blockIdx.x) * CACHE_THREADS + threadIdx.x;
-  const Item it = item_of(tid / LANES, p.Hkv);
-  const int j = static_cast<int>(tid % LANES);
-  const bool in = it.token < p.T && it.head < p.Hkv;
-  long long slot = in ? p.slots[it.token] : -1;
-  if (slot >= p.num_slots || slot < -1) {
-    kv4_record(&g_kv4_cache_status, RA_ERR_INVALID_ARG, KV4_SITE_SLOT);
-    slot = -1;
+  using C = CacheCta<D>;
+  constexpr int LANES = C::LANES;
+  const Place at = place_of<D>(p.Hkv);
+  const int j = at.lane;
+  uint4 k[HEADS_AT_ONCE], v[HEADS_AT_ONCE];
+#pragma unroll
+  for (int u = 0; u < HEADS_AT_ONCE; ++u) {
+    const int head = at.head0 + u * C::ACROSS;
+    k[u] = v[u] = make_uint4(0, 0, 0, 0);
+    if (at.token < p.T && head < p.Hkv) {
+      k[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.k) + at.token * p.k_stride +
+                                             head * D + j * 8);
+      v[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + at.token * p.v_stride +
+                                             head * D + j * 8);
+    }
   }
-  const bool use = slot >= 0;
-  uint4 k = make_uint4(0, 0, 0, 0), v = k;
-  if (use) {
-    k = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.k) + it.token * p.k_stride +
-                                        it.head * D + j * 8);
-    v = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + it.token * p.v_stride +
-                                        it.head * D + j * 8);
-  }
-  const uint2 kc = kv4_encode8<T, LANES>(k);
-  const uint2 vc = kv4_encode8<T, LANES>(v);
-  // neighbouring items are neighbouring tokens of one head; if their slots are
-  // an even one and the next, their V codes share words
-  const int side = it.token & 1;
-  const uint32_t other = __shfl_xor_sync(0xffffffffu, vc.x, LANES);
-  const long long slot2 = __shfl_xor_sync(0xffffffffu, slot, LANES);
-  const bool paired = slot >= 0 && slot2 >= 0 && (slot & 1) == side &&
-                      (side == 0 ? slot2 == slot + 1 : slot2 == slot - 1);
-  if (!use) return;
-  const long long page = slot / p.page;
-  const int o = static_cast<int>(slot - page * p.page);
-  const int i = o & 15;
-  uint8_t* blk = p.cache + ((page * p.Hkv + it.head) * (p.page >> 4) + (o >> 4)) * L::BLOCK_BYTES;
-  *reinterpret_cast<uint32_t*>(blk + i * L::ROW + j * 4) = kc.x;
-  uint8_t* vb = blk + L::OFF_V;
-  if (paired) {
-    // both tokens of a word in this warp: each lane stores one whole word
-    const uint32_t word = side == 0 ? __byte_perm(vc.x, other, 0x5410)
-                                    : __byte_perm(vc.x, other, 0x3276);
-    *reinterpret_cast<uint32_t*>(vb + L::v_code_offset(i & ~1, 2 * j + side)) = word;
-  } else {
-    *reinterpret_cast<uint16_t*>(vb + L::v_code_offset(i, 2 * j)) = static_cast<uint16_t>(vc.x);
-    *reinterpret_cast<uint16_t*>(vb + L::v_code_offset(i, 2 * j + 1)) =
-        static_cast<uint16_t>(vc.x >> 16);
-  }
-  if (j == 0) {
-    *reinterpret_cast<uint32_t*>(blk + L::OFF_KP + 4 * i) = kc.y;
-    *reinterpret_cast<uint32_t*>(blk + L::OFF_VP + 4 * i) = vc.y;
+  const int slot = slot_of(p, at.token);
+  // neighbouring vectors of the warp are neighbouring tokens of a head; if
+  // their slots are an even one and the next, their V codes share words
+  const int side = static_cast<int>(at.token) & 1;
+  const int slot2 = __shfl_xor_sync(0xffffffffu, slot, LANES);
+  const bool paired = slot >= 0 && (slot & 1) == side && slot2 == (slot ^ 1);
+  const unsigned page = max(slot, 0) / static_cast<unsigned>(p.page);
+  const int o = max(slot, 0) - page * p.page, i = o & 15;
+#pragma unroll
+  for (int u = 0; u < HEADS_AT_ONCE; ++u) {
+    const int head = at.head0 + u * C::ACROSS;
+    const uint2 kc = kv4_encode8<T, LANES>(k[u]);
+    const uint2 vc = kv4_encode8<T, LANES>(v[u]);
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, vc.x, LANES);
+    if (slot < 0 || head >= p.Hkv) continue;
+    uint8_t* blk = p.cache + ((static_cast<long long>(page) * p.Hkv + head) * (p.page >> 4) +
+                              (o >> 4)) * L::BLOCK_BYTES;
+    *reinterpret_cast<uint32_t*>(blk + i * L::ROW + j * 4) = kc.x;
+    uint8_t* vb = blk + L::OFF_V;
+    if (paired) {
+      // both tokens of a word in this warp: each lane stores one whole word
+      const uint32_t word = side == 0 ? __byte_perm(vc.x, other, 0x5410)
+                                      : __byte_perm(vc.x, other, 0x3276);
+      *reinterpret_cast<uint32_t*>(vb + L::v_code_offset(i & ~1, 2 * j + side)) = word;
+    } else {
+      *reinterpret_cast<uint16_t*>(vb + L::v_code_offset(i, 2 * j)) = static_cast<uint16_t>(vc.x);
+      *reinterpret_cast<uint16_t*>(vb + L::v_code_offset(i, 2 * j + 1)) =
+          static_cast<uint16_t>(vc.x >> 16);
+    }
+    if (j == 0) {
+      *reinterpret_cast<uint32_t*>(blk + L::OFF_KP + 4 * i) = kc.y;
+      *reinterpret_cast<uint32_t*>(blk + L::OFF_VP + 4 * i) = vc.y;
+    }
   }
 }
 
@@ -414,43 +458,48 @@ __device__ __forceinline__ void decode8(T* dst, uint32_t codes, uint32_t params)
 template <int D, class T>
 __global__ void __launch_bounds__(CACHE_THREADS) ra_kv4_read_kernel(const Kv4CopyParams p) {
   using L = Kv4<D>;
-  constexpr int LANES = D / 8;
-  const long long tid = static_cast<long long>(blockIdx.x) * CACHE_THREADS + threadIdx.x;
-  const Item it = item_of(tid / LANES, p.Hkv);
-  const int j = static_cast<int>(tid % LANES);
-  if (it.token >= p.T || it.head >= p.Hkv) return;
-  long long slot = p.slots[it.token];
-  if (slot >= p.num_slots || slot < -1) {
-    kv4_record(&g_kv4_cache_status, RA_ERR_INVALID_ARG, KV4_SITE_SLOT);
-    slot = -1;
+  using C = CacheCta<D>;
+  const Place at = place_of<D>(p.Hkv);
+  const int j = at.lane;
+  if (at.token >= p.T) return;
+  const int slot = slot_of(p, at.token);
+  const unsigned page = max(slot, 0) / static_cast<unsigned>(p.page);
+  const int o = max(slot, 0) - page * p.page, i = o & 15;
+  uint32_t kc[HEADS_AT_ONCE], vc[HEADS_AT_ONCE], kp[HEADS_AT_ONCE], vp[HEADS_AT_ONCE];
+#pragma unroll
+  for (int u = 0; u < HEADS_AT_ONCE; ++u) {
+    const int head = at.head0 + u * C::ACROSS;
+    kc[u] = vc[u] = kp[u] = vp[u] = 0;
+    if (slot >= 0 && head < p.Hkv) {
+      const uint8_t* blk = p.cache + ((static_cast<long long>(page) * p.Hkv + head) *
+                                          (p.page >> 4) + (o >> 4)) * L::BLOCK_BYTES;
+      kc[u] = *reinterpret_cast<const uint32_t*>(blk + i * L::ROW + j * 4);
+      const uint8_t* vb = blk + L::OFF_V;
+      // the words with the token's halves of elements 8 j .. 8 j + 7, side by
+      // side with those of its neighbour's
+      const uint32_t w0 = *reinterpret_cast<const uint32_t*>(vb + L::v_code_offset(i & ~1, 2 * j));
+      const uint32_t w1 =
+          *reinterpret_cast<const uint32_t*>(vb + L::v_code_offset(i & ~1, 2 * j + 1));
+      vc[u] = __byte_perm(w0, w1, (i & 1) ? 0x7632 : 0x5410);
+      kp[u] = *reinterpret_cast<const uint32_t*>(blk + L::OFF_KP + 4 * i);
+      vp[u] = *reinterpret_cast<const uint32_t*>(blk + L::OFF_VP + 4 * i);
+    }
   }
-  const bool use = slot >= 0;
-  uint32_t kc = 0, vc = 0, kp = 0, vp = 0;
-  if (use) {
-    const long long page = slot / p.page;
-    const int o = static_cast<int>(slot - page * p.page);
-    const int i = o & 15;
-    const uint8_t* blk =
-        p.cache + ((page * p.Hkv + it.head) * (p.page >> 4) + (o >> 4)) * L::BLOCK_BYTES;
-    kc = *reinterpret_cast<const uint32_t*>(blk + i * L::ROW + j * 4);
-    const uint8_t* vb = blk + L::OFF_V;
-    vc = *reinterpret_cast<const uint16_t*>(vb + L::v_code_offset(i, 2 * j)) |
-         (static_cast<uint32_t>(
-              *reinterpret_cast<const uint16_t*>(vb + L::v_code_offset(i, 2 * j + 1)))
-          << 16);
-    kp = *reinterpret_cast<const uint32_t*>(blk + L::OFF_KP + 4 * i);
-    vp = *reinterpret_cast<const uint32_t*>(blk + L::OFF_VP + 4 * i);
+#pragma unroll
+  for (int u = 0; u < HEADS_AT_ONCE; ++u) {
+    const int head = at.head0 + u * C::ACROSS;
+    if (head >= p.Hkv) continue;
+    const long long dst = (at.token * p.Hkv + head) * D + j * 8;
+    decode8(static_cast<T*>(p.k_out) + dst, kc[u], kp[u]);
+    decode8(static_cast<T*>(p.v_out) + dst, vc[u], vp[u]);
   }
-  const long long dst = (it.token * p.Hkv + it.head) * D + j * 8;
-  decode8(static_cast<T*>(p.k_out) + dst, kc, kp);
-  decode8(static_cast<T*>(p.v_out) + dst, vc, vp);
 }
 
-template <class F>
-cudaError_t launch_copy(F kernel, const Kv4CopyParams& p, int d, cudaStream_t stream) {
+template <int D>
+cudaError_t launch_copy(void (*kernel)(const Kv4CopyParams), const Kv4CopyParams& p,
+                        cudaStream_t stream) {
   const long long groups = (p.T + 15) / 16;
-  const long long threads = groups * 16 * p.Hkv * (d / 8);
-  const long long grid = (threads + CACHE_THREADS - 1) / CACHE_THREADS;
+  const long long grid = groups * ((p.Hkv + CacheCta<D>::HEADS - 1) / CacheCta<D>::HEADS);
   if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   kernel<<<static_cast<unsigned>(grid), CACHE_THREADS, 0, stream>>>(p);
   return cudaGetLastError();
@@ -488,21 +537,21 @@ cudaError_t launch_kv4_plan(const Kv4PlanParams& p, cudaStream_t stream) {
 
 cudaError_t launch_kv4_append(const Kv4CopyParams& p, int d, int dtype, cudaStream_t stream) {
   if (dtype == RA_BF16)
-    return d == 128 ? launch_copy(ra_kv4_append_kernel<128, __nv_bfloat16>, p, d, stream)
-                    : launch_copy(ra_kv4_append_kernel<64, __nv_bfloat16>, p, d, stream);
-  return d == 128 ? launch_copy(ra_kv4_append_kernel<128, __half>, p, d, stream)
-                  : launch_copy(ra_kv4_append_kernel<64, __half>, p, d, stream);
+    return d == 128 ? launch_copy<128>(ra_kv4_append_kernel<128, __nv_bfloat16>, p, stream)
+                    : launch_copy<64>(ra_kv4_append_kernel<64, __nv_bfloat16>, p, stream);
+  return d == 128 ? launch_copy<128>(ra_kv4_append_kernel<128, __half>, p, stream)
+                  : launch_copy<64>(ra_kv4_append_kernel<64, __half>, p, stream);
 }
 
 cudaError_t launch_kv4_read(const Kv4CopyParams& p, int d, int dtype, cudaStream_t stream) {
   if (dtype == RA_BF16)
-    return d == 128 ? launch_copy(ra_kv4_read_kernel<128, __nv_bfloat16>, p, d, stream)
-                    : launch_copy(ra_kv4_read_kernel<64, __nv_bfloat16>, p, d, stream);
+    return d == 128 ? launch_copy<128>(ra_kv4_read_kernel<128, __nv_bfloat16>, p, stream)
+                    : launch_copy<64>(ra_kv4_read_kernel<64, __nv_bfloat16>, p, stream);
   if (dtype == RA_FP16)
-    return d == 128 ? launch_copy(ra_kv4_read_kernel<128, __half>, p, d, stream)
-                    : launch_copy(ra_kv4_read_kernel<64, __half>, p, d, stream);
-  return d == 128 ? launch_copy(ra_kv4_read_kernel<128, float>, p, d, stream)
-                  : launch_copy(ra_kv4_read_kernel<64, float>, p, d, stream);
+    return d == 128 ? launch_copy<128>(ra_kv4_read_kernel<128, __half>, p, stream)
+                    : launch_copy<64>(ra_kv4_read_kernel<64, __half>, p, stream);
+  return d == 128 ? launch_copy<128>(ra_kv4_read_kernel<128, float>, p, stream)
+                  : launch_copy<64>(ra_kv4_read_kernel<64, float>, p, stream);
 }
 
 cudaError_t read_and_clear_kv4_cache_status(unsigned long long* out) {
