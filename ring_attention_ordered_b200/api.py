@@ -316,6 +316,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 class _Here:
     """``_on`` where nothing has to be switched: the tensors' device is the
     current one and the call uses its current stream."""
@@ -334,7 +337,7 @@ class _Here:
 
 def _here(device, stream):
     index = device.index
-    if stream is None and torch.cuda.current_device() == index:
+    if stream is None and _current_device() == index:
         return _Here(_raw_stream(index))
     return _on(device, stream)
 
@@ -435,11 +438,8 @@ def kv4_plan(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, pool: t
         raise ValueError(f"max_tokens must be >= 0, got {max_tokens}")
     with _here(dev, stream) as sh:
         if out is None:
-            # one allocation, each part on a 16-byte boundary
-            sizes = [-(-n // 4) * 4 for n in (R * W, num_pages + 1, max_tokens, R, R + 1, 1)]
-            b = torch.empty(sum(sizes), dtype=i32, device=dev).split(sizes)
-            out = (b[3][:R], b[0][:R * W].view(R, W), b[1][:num_pages + 1], b[4][:R + 1],
-                   b[2][:max_tokens], b[5][:1])
+            out = [torch.empty(shape, dtype=i32, device=dev)
+                   for shape in (R, (R, W), num_pages + 1, R + 1, max_tokens, 1)]
         else:
             for t, n, shape in zip(out, ("lens", "table", "pool", "cu", "slots", "shortage"),
                                    ((R,), (R, W), (num_pages + 1,), (R + 1,), (max_tokens,), (1,)),

@@ -197,7 +197,6 @@ struct Kv4AttnParams {
   // rows_min 0: every request is the chunk kernel's
   int rows_min, rows_max;
   int cell_shift;         // decoding: see Kv4Line
-  int few_units;          // decoding: the units, if they are few, else 0
   unsigned* counters;     // workspace: zero before and after the launch
   float* partials;        // workspace
   unsigned long long wait_limit_ns;

@@ -127,10 +127,10 @@ __device__ __forceinline__ void kv4_merge(float& m, float& l, float4& a, float m
 
 // Store four elements of a finished row: a / l, or zeros if the row saw no
 // token, and by the row's first lane lse = (m + log2 l) ln 2, or -inf.
-__device__ __forceinline__ void kv4_store(const Kv4AttnParams& p, const Kv4Req& q, int h, int row,
-                                          int d0, int d, float4 a, float m, float l) {
+__device__ __forceinline__ void kv4_store(const Kv4AttnParams& p, int first, int h, int row, int d0,
+                                          int d, float4 a, float m, float l) {
   const int tok = row / p.group, head = h * p.group + (row - tok * p.group);
-  const long long at = (static_cast<long long>(q.first) + tok) * p.Hq + head;
+  const long long at = (static_cast<long long>(first) + tok) * p.Hq + head;
   const bool none = l == 0.f;
   const float inv = 1.f / l;
   const float4 y = none ? make_float4(0.f, 0.f, 0.f, 0.f)
@@ -179,10 +179,14 @@ __device__ __noinline__ void kv4_fill_empty(const Kv4AttnParams& p, unsigned lon
 // blocks, and as many as bring it to a multiple of `align`.  The warps of the
 // launch take equal stretches of `per` cells.
 //
-// Packed (lead > 0, align 1): every warp the same share of the work.  Aligned
-// (lead 0, align a CTA's stretch), for few units: each starts with a CTA, so
-// that a short one is finished in its CTA, and what is left empty behind the
-// units' ends is little beside the whole.
+// Packed (lead > 0, align 1): every warp the same share of the work, whatever
+// the lengths; but units then cross warps and CTAs where it happens.  Aligned
+// (lead 0): every unit starts at a multiple of `align` cells, the stretches of
+// 1, 2, 4 or 8 warps, so that it stays in those, or, being longer, in whole CTAs.
+// Chosen where the longest stretch grows by 6 cells and a 32nd at most: that is
+// about what pieces that cross CTAs cost (measured: 296 units of 256 blocks 49 us
+// packed, 39 us aligned; 256 units of 2000 blocks 193 us packed, 218 us aligned,
+// a stretch longer by 15%).
 //
 // Cell numbers are 32 bits wide: the host chooses `shift` so that the longest
 // line the arguments allow stays below 2^31.
@@ -224,9 +228,38 @@ __device__ __forceinline__ int kv4_warp_scan(int x) {
   return x;
 }
 
+// Cells of a warp's stretch, packed; and the alignment (0: none) and cells of
+// one in which `units` units, the longest of `most` cells and `total` in all,
+// start in warps of their own.
+struct Kv4Layout {
+  int per, align;
+};
+template <int WARPS>
+__device__ __forceinline__ Kv4Layout kv4_layout(int units, int most, int total, int packed,
+                                                int warps, int min_cells) {
+  const int per = max((packed + warps - 1) / warps, min_cells);
+  if (units == 0 || units > warps) return {per, 0};
+  int per2, align;
+  const int each = warps / units;           // warps a unit
+  if (each < WARPS) {
+    const int a = each >= 4 && WARPS > 4 ? 4 : each >= 2 ? 2 : 1;
+    per2 = (most + a - 1) / a;
+    align = a;
+  } else {
+    // the same number of CTAs for each, or one stretch each left partly empty
+    const int ctas = warps / WARPS, same = ctas / units * WARPS;
+    per2 = (most + same - 1) / same;
+    if (units < ctas) per2 = min(per2, (total + (ctas - units) * WARPS - 1) / ((ctas - units) * WARPS));
+    align = WARPS;
+  }
+  per2 = max(per2, min_cells);
+  if (per2 > per + per / 32 + 6) return {per, 0};
+  return {per2, align * per2};
+}
+
 // Lays the line out and finds where warp `me` of the launch's `warps` begins.
 // Up to 32 requests each warp does so by itself; more are taken a thread at a
-// time by the CTA (s_scan: WARPS ints, s_start: one a warp).
+// time by the CTA (s_scan: 3 WARPS ints, s_start: one a warp).
 template <int ROWS, int WARPS>
 __device__ __forceinline__ Kv4Start kv4_find_start(const Kv4AttnParams& p, int lead, int min_cells,
                                                    int me, int warps, int* s_scan,
@@ -235,20 +268,24 @@ __device__ __forceinline__ Kv4Start kv4_find_start(const Kv4AttnParams& p, int l
   line.shift = p.cell_shift;
   line.lead = lead;
   line.align = 1;
-  auto stretch = [&] { return max((line.total + warps - 1) / warps, min_cells); };
+  auto lay_out = [&](int units, int most, int packed) {
+    const Kv4Layout x = kv4_layout<WARPS>(units, most, packed - units * lead, packed, warps,
+                                          min_cells);
+    line.per = x.per;
+    if (x.align) {
+      line.lead = 0;
+      line.align = x.align;
+    }
+    return x.align != 0;
+  };
   if (p.R <= 32) {
     const Kv4Load x = kv4_load<ROWS>(p, lane);
     line.odd = __any_sync(0xffffffffu, x.odd);
     int all = line.cells(x.nb);
     int hi = kv4_warp_scan(x.units * all);
     line.total = __shfl_sync(0xffffffffu, hi, 31);
-    line.per = stretch();
-    if (__reduce_add_sync(0xffffffffu, x.units) <= p.few_units) {
-      // as many stretches as units may be left partly empty
-      const int ctas = warps / WARPS - p.few_units;
-      line.per = max((line.total + ctas * WARPS - 1) / (ctas * WARPS), min_cells);
-      line.lead = 0;
-      line.align = line.per * WARPS;
+    if (lay_out(__reduce_add_sync(0xffffffffu, x.units),
+                __reduce_max_sync(0xffffffffu, x.units ? all - lead : 0), line.total)) {
       all = line.cells(x.nb);
       hi = kv4_warp_scan(x.units * all);
       line.total = __shfl_sync(0xffffffffu, hi, 31);
@@ -264,24 +301,51 @@ __device__ __forceinline__ Kv4Start kv4_find_start(const Kv4AttnParams& p, int l
   }
   // thread tid: requests [tid * each, tid * each + each)
   const int each = (p.R + WARPS * 32 - 1) / (WARPS * 32);
-  int mine = 0;
+  int mine = 0, units = 0, most = 0;
   bool odd = false;
   for (int i = 0; i < each; ++i) {
     const Kv4Load x = kv4_load<ROWS>(p, tid * each + i);
     mine += x.units * line.cells(x.nb);
+    units += x.units;
+    if (x.units) most = max(most, line.cells(x.nb) - lead);
     odd |= x.odd;
   }
-  const int inc = kv4_warp_scan(mine);
-  if (lane == 31) s_scan[warp] = inc;
+  int inc = kv4_warp_scan(mine);
+  units = __reduce_add_sync(0xffffffffu, units);
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) {
+    s_scan[warp] = inc;
+    s_scan[WARPS + warp] = units;
+    s_scan[2 * WARPS + warp] = most;
+  }
   line.odd = __syncthreads_or(odd);
   int lo = inc - mine;
-  line.total = 0;
+  line.total = units = most = 0;
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) {
     if (w < warp) lo += s_scan[w];
     line.total += s_scan[w];
+    units += s_scan[WARPS + w];
+    most = max(most, s_scan[2 * WARPS + w]);
   }
-  line.per = stretch();
+  if (lay_out(units, most, line.total)) {
+    __syncthreads();
+    mine = 0;
+    for (int i = 0; i < each; ++i) {
+      const Kv4Load x = kv4_load<ROWS>(p, tid * each + i);
+      mine += x.units * line.cells(x.nb);
+    }
+    inc = kv4_warp_scan(mine);
+    if (lane == 31) s_scan[warp] = inc;
+    __syncthreads();
+    lo = inc - mine;
+    line.total = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) lo += s_scan[w];
+      line.total += s_scan[w];
+    }
+  }
   // the first of this CTA's warps that begins behind `lo`
   const int me0 = me - warp;
   int x = max((lo + line.per - 1) / line.per - me0, 0);

@@ -656,10 +656,6 @@ __device__ __noinline__ int fold(const Kv4AttnParams& p, const Piece* piece, int
                                  int n, bool starts, bool finish, RowSync sync, Ctl cx) {
   constexpr int LPR = D / 4, RPR = 256 / LPR, V = 8;   // rows a round, rows a thread
   const Piece x = *piece;
-  Kv4Req q;
-  q.first = x.first;
-  q.n = x.n;
-  q.len = x.len;
   const int rows = min(UNIT_ROWS, x.rows - x.row0);
   const int d = 4 * (threadIdx.x % LPR);
 #pragma unroll 1
@@ -699,7 +695,7 @@ __device__ __noinline__ int fold(const Kv4AttnParams& p, const Piece* piece, int
       const int row = r0 + v * RPR;
       if (row >= rows) continue;
       if (finish) {
-        kv4_store(p, q, x.h, x.row0 + row, d, D, a[v], m[v] - P_SHIFT, ls[v]);
+        kv4_store(p, x.first, x.h, x.row0 + row, d, D, a[v], m[v] - P_SHIFT, ls[v]);
       } else {
         float* dst = p.partials + (2ll * c0 + starts) * KV4C_PIECE_FLOATS;
         *reinterpret_cast<float4*>(dst + row * D + d) = a[v];
@@ -880,7 +876,7 @@ __device__ void softmax_role(const Kv4AttnParams& p, const Bars& br, uint32_t ba
                                    __uint_as_float(o[j + 2]), __uint_as_float(o[j + 3]));
             if (bad) a.x = a.y = a.z = a.w = __uint_as_float(0x7fffffffu);
             if (whole)
-              kv4_store(p, q, h, row, cc * 32 + j, D, a, m - P_SHIFT, l);
+              kv4_store(p, q.first, h, row, cc * 32 + j, D, a, m - P_SHIFT, l);
             else
               *reinterpret_cast<float4*>(slot + lrow * D + cc * 32 + j) = a;
           }

@@ -62,7 +62,7 @@ namespace kv4d {
 #define KV4_MINC 8
 #endif
 #ifndef KV4_UC
-#define KV4_UC 4
+#define KV4_UC 8
 #endif
 #ifndef KV4_STAGES
 #define KV4_STAGES 2
@@ -135,23 +135,21 @@ __device__ __forceinline__ void code_pairs(uint32_t x, uint32_t (&p)[4]) {
   p[3] = y & 0x00f000f0u;
 }
 
-// A unit of which this CTA holds pieces: the warps of the launch w0 .. w1.
+// A unit of which this CTA holds pieces: where its rows are, and the warps w0
+// .. w1 of the launch.
 struct Group {
-  int r, unit, w0, w1;
+  int n_rows, first, h, row0, w0, w1;
 };
 
 // Pieces of unit u in the workspace, of the CTAs c0 + i step, i < n, folded in
 // that order: stored as the result, or as the piece of the first of them.
 // s_part: shared memory for [parts][items][a, m, l].
 template <int D, int NT>
-__device__ __noinline__ void kv4_fold(const Kv4AttnParams& p, int r, int unit, int c0, int step,
-                                      int n, bool starts, bool finish, float* s_part) {
+__device__ __noinline__ void kv4_fold(const Kv4AttnParams& p, const Group u, int c0, int step, int n,
+                                      bool starts, bool finish, float* s_part) {
   constexpr int ROWS = 8 * NT, LPR = D / 4;
   const int tid = threadIdx.x;
-  const Kv4Req q = kv4_request(p, r);
-  const int rows = q.n * p.group, tiles = (rows + ROWS - 1) / ROWS;
-  const int h = unit / tiles, row0 = (unit - h * tiles) * ROWS;
-  const int items = min(ROWS, rows - row0) * LPR;
+  const int items = u.n_rows * LPR;
   // Part y of the threads folds every parts-th piece of (row, 4 elements) x,
   // with all loads of a round in flight; then the parts are merged.
   const int parts = max(THREADS / items, 1);
@@ -197,7 +195,7 @@ __device__ __noinline__ void kv4_fold(const Kv4AttnParams& p, int r, int unit, i
       kv4_merge(m, ls, a, src[4], src[5], *reinterpret_cast<const float4*>(src));
     }
     if (finish) {
-      kv4_store(p, q, h, row0 + row, d, D, a, m - P_SHIFT, ls);
+      kv4_store(p, u.first, u.h, u.row0 + row, d, D, a, m - P_SHIFT, ls);
     } else {
       float* dst = p.partials + (2ll * c0 + starts) * KV4_PIECE_FLOATS;
       *reinterpret_cast<float4*>(dst + row * D + d) = a;
@@ -235,7 +233,7 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
   __shared__ uint32_t s_abort;
   __shared__ int s_last;
   __shared__ Kv4Start s_start[WARPS];
-  __shared__ int s_scan[WARPS];
+  __shared__ int s_scan[3 * WARPS];
   __shared__ Group s_group[WARPS + 1];   // 0: the CTA's first piece, 1 + w: warp w's tail
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -248,7 +246,7 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
   const Ctl cx{&s_abort, p.wait_limit_ns, &g_status};
 
   if (tid == 0) s_abort = 0u;
-  if (tid <= WARPS) s_group[tid].r = -1;
+  if (tid <= WARPS) s_group[tid].n_rows = 0;
   if (lane == 0) {
     for (int i = 0; i < STAGES; ++i) mbar_init(bars + 8 * i, 1);
     fence_mbarrier_init();
@@ -593,7 +591,7 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
           if (row < rows)
 #pragma unroll
             for (int w = 0; w < WPL; ++w)
-              kv4_store(p, q, h, row, g * (D / 8) + 4 * w, D, values(j, cc, w), -mo[j][cc], l[j][cc]);
+              kv4_store(p, q.first, h, row, g * (D / 8) + 4 * w, D, values(j, cc, w), -mo[j][cc], l[j][cc]);
         }
       continue;
     }
@@ -614,14 +612,14 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
         }
       }
     if (lane == 0 && (!head || warp == 0)) 
-      s_group[head ? 0 : 1 + warp] = {r, here, first / per, last / per};
+      s_group[head ? 0 : 1 + warp] = {min(ROWS, rows - row0), q.first, h, row0, first / per, last / per};
   }
 
   // ---- units that cross warps: merged by the CTA, a row to a warp at a time
   __syncthreads();
   if (s_abort) return;
   const int cta0 = blockIdx.x * WARPS;
-  const unsigned groups = __ballot_sync(0xffffffffu, lane <= WARPS && s_group[min(lane, WARPS)].r >= 0);
+  const unsigned groups = __ballot_sync(0xffffffffu, lane <= WARPS && s_group[min(lane, WARPS)].n_rows > 0);
   unsigned crossing = 0;                 // groups that other CTAs hold pieces of
   constexpr int LPR = D / 4;             // lanes of a row
   constexpr int RPW = 32 / LPR;          // rows a warp takes at once
@@ -630,10 +628,7 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
   for (unsigned rest = groups; rest != 0; rest &= rest - 1) {
     const int k = __ffs(rest) - 1;
     const Group u = s_group[k];
-    const Kv4Req q = kv4_request(p, u.r);
-    const int rows = q.n * p.group, tiles = (rows + ROWS - 1) / ROWS;
-    const int h = u.unit / tiles, row0 = (u.unit - h * tiles) * ROWS;
-    const int n_rows = min(ROWS, rows - row0);
+    const int n_rows = u.n_rows;
     const int lo = max(u.w0 - cta0, 0), hi = min(u.w1 - cta0, WARPS - 1);
     const int c0 = u.w0 / WARPS, c1 = u.w1 / WARPS;
     if (c0 != c1) crossing |= 1u << k;
@@ -652,7 +647,7 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
                   *reinterpret_cast<const float4*>(piece_at(w, head) + row * S::RS + d4));
       }
       if (c0 == c1) {
-        kv4_store(p, q, h, row0 + row, d4, D, a, m - P_SHIFT, ls);
+        kv4_store(p, u.first, u.h, u.row0 + row, d4, D, a, m - P_SHIFT, ls);
       } else {
         *reinterpret_cast<float4*>(slot + row * D + d4) = a;
         if (d4 == 0) {
@@ -675,10 +670,10 @@ __global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
     const bool starts = sub == 0;
     if (!kv4_last(p.counters + 2 * first + starts, n, &s_last)) continue;
     const bool one = c1 - c0 < FOLD;
-    kv4_fold<D, NT>(p, u.r, u.unit, first, 1, n, starts, one, s_part);
+    kv4_fold<D, NT>(p, u, first, 1, n, starts, one, s_part);
     const int subs = (c1 - c0) / FOLD + 1;
     if (one || !kv4_last(p.counters + 2 * KV4_MAX_CTAS + c0, subs, &s_last)) continue;
-    kv4_fold<D, NT>(p, u.r, u.unit, c0, FOLD, subs, true, true, s_part);
+    kv4_fold<D, NT>(p, u, c0, FOLD, subs, true, true, s_part);
   }
   if (line.odd) kv4_fill_empty<D, THREADS>(p, &g_status);
 }
@@ -700,14 +695,12 @@ cudaError_t launch(Kv4AttnParams p, int num_sms, int max_ctas, cudaStream_t stre
   int grid = num_sms * ((NT == 1 ? 16 : 8) / WARPS);
   if (max_ctas > 0 && max_ctas < grid) grid = max_ctas;
   if (grid > KV4_MAX_CTAS) grid = KV4_MAX_CTAS;
-  // units, and with the longest requests the table can name, cells at most;
-  // half a sixteenth of the line is what aligned units leave empty at most
-  const long long tiles = static_cast<long long>(p.T) * p.group / S::ROWS + p.R;
-  const double units = static_cast<double>(tiles) * p.Hkv;
-  p.few_units = p.R <= 32 && units * 16 <= grid ? static_cast<int>(units) : 0;
-  const double blocks = static_cast<double>(p.W) * p.page / KV4_BLOCK;
+  // no more units, and with the longest requests the table can name cells,
+  // than these (aligned units are padded to four times their cells at most)
+  const double units = (static_cast<double>(p.T) * p.group / S::ROWS + p.R) * p.Hkv;
+  const double blocks = 4.0 * p.W * p.page / KV4_BLOCK;
   p.cell_shift = 0;
-  while (units * (blocks / (1ll << p.cell_shift) + UNIT_COST + 1) >= 2e9) ++p.cell_shift;
+  while (units * (blocks / (1ll << p.cell_shift) + UNIT_COST + MIN_CELLS * WARPS) >= 2e9) ++p.cell_shift;
   ra_kv4_decode_kernel<D, NT><<<grid, THREADS, S::BYTES, stream>>>(p);
   return cudaGetLastError();
 }
