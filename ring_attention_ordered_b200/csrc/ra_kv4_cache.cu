@@ -235,41 +235,49 @@ __device__ __forceinline__ uint32_t as_word(T2 x) {
 }
 
 // The code of one value: the nearest level of 0..15 to (x - zero) / step,
-// ties to the even code.  The quotient by the rounded reciprocal is within
-// 4 ulp of 16 (2^-18) of the exact one, so only a value within 2^-16 of a
-// border can fall on the wrong side; those compare x with the border
-// zero + (n + 1/2) step, which is exact in fp64 (multiples of 2^-25 below
-// 2^17).
+// ties to the even code.  n is a level within one of it; the residual
+// r = a - n step with a = x - zero rounded is exact (n step has 15 bits, and r
+// is a multiple of a's last place no larger than step), and e is what the
+// rounding of a left out, which decides where r lies on a border.
 __device__ __forceinline__ uint32_t kv4_code(float x, float zero, float step, float inv) {
-  const float t = fminf(fmaxf((x - zero) * inv, 0.f), 15.f);
-  const float n = floorf(t);
-  uint32_t c = static_cast<uint32_t>(n);
-  const float f = t - n;
-  if (fabsf(f - 0.5f) < 1.52587890625e-5f) {
-    const double border = static_cast<double>(zero) +
-                          (static_cast<double>(n) + 0.5) * static_cast<double>(step);
-    const double d = static_cast<double>(x) - border;
-    c += d > 0.0 ? 1u : d == 0.0 ? (c & 1u) : 0u;
-  } else {
-    c += f > 0.5f ? 1u : 0u;
-  }
-  return c;
+  const float a = x - zero, b = a - x;
+  const float e = (x - (a - b)) - (zero + b);
+  const float n = rintf(fminf(fmaxf(a * inv, 0.f), 15.f));
+  const float r = fmaf(-n, step, a), half = 0.5f * step;
+  const bool odd = (static_cast<int>(n) & 1) != 0;
+  const bool up = r > half || (r == half && (e > 0.f || (e == 0.f && odd)));
+  const bool down = r < -half || (r == -half && (e < 0.f || (e == 0.f && odd)));
+  return static_cast<uint32_t>(min(max(static_cast<int>(n) + up - down, 0), 15));
 }
 
-// Eight values of one lane; the LANES lanes of the vector agree on its range.
-// Returns the codes (element i in nibble i) and the parameter word.
+// Sixteen values of one lane; the LANES lanes of the vector agree on its
+// range.  `use`: whether anything is made of the result.  Returns the codes (element i in nibble i) and the parameter word.
 //
-// Almost always the codes come from t = (x - zero) * (1 / step) rounded to an
-// integer by adding 1.5 * 2^23, four codes joined as one float below 2^24.  A
-// lane with a value near a border takes kv4_code for its eight, and so does a
-// vector in which t may leave [0, 15]: a step so small that rounding it or the
-// zero to fp16's subnormals counts, or values that were clamped.
+// The codes come from t = (x - zero) / step rounded to an integer by adding 1.5
+// * 2^23, four codes joined as one float below 2^24.  The quotient by the
+// approximate reciprocal (one ulp) is within 15 * 2^-22 of the exact one, so
+// only a value within 2^-17 of a border can be wrong; a lane that has one (one
+// in 90 does: values and steps of few bits often lie exactly half way) takes
+// kv4_code for its own, and so does a vector in which t may leave [0, 15]: a
+// step so small that rounding it or the zero to fp16's subnormals counts, or
+// values that were clamped.
+//
+// The quotient (max - min) / 15 is formed by Markstein's method, a product by
+// the rounded reciprocal and one correction, which gives the correctly rounded
+// one (checked for every significand in nine binades).
+struct Kv4Codes {
+  uint32_t lo, hi, params;
+};
 template <class T, int LANES>
-__device__ __forceinline__ uint2 kv4_encode8(uint4 x) {
+__device__ __forceinline__ Kv4Codes kv4_encode16(uint4 x, uint4 y, bool use) {
   using T2 = typename Pair<T>::T2;
-  const T2 a = as_pair<T2>(x.x), b = as_pair<T2>(x.y), c = as_pair<T2>(x.z), d = as_pair<T2>(x.w);
-  const T2 mn = __hmin2_nan(__hmin2_nan(a, b), __hmin2_nan(c, d));
-  const T2 mx = __hmax2_nan(__hmax2_nan(a, b), __hmax2_nan(c, d));
+  const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  T2 mn = as_pair<T2>(w[0]), mx = mn;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    mn = __hmin2_nan(mn, as_pair<T2>(w[i]));
+    mx = __hmax2_nan(mx, as_pair<T2>(w[i]));
+  }
   // (min, -max) in one word: both are minima, exact in the input's type
   const uint32_t mnw = as_word<T2>(mn), mxw = as_word<T2>(mx) ^ 0x80008000u;
   T2 m = __hmin2_nan(as_pair<T2>(__byte_perm(mnw, mxw, 0x5410)),
@@ -281,57 +289,76 @@ __device__ __forceinline__ uint2 kv4_encode8(uint4 x) {
   const bool nan = r.x != r.x;   // a NaN reaches both halves
   const float lo = fminf(fmaxf(r.x, -65504.f), 65504.f);
   const float hi = fminf(fmaxf(-r.y, -65504.f), 65504.f);
+  const float span = hi - lo;
+  constexpr float FIFTEENTH = 1.f / 15.f;
+  const float q0 = span * FIFTEENTH;
   const __half zh = __float2half_rn(lo);
-  __half sh = __float2half_rz(__fdiv_rn(hi - lo, 15.f));
+  __half sh = __float2half_rz(fmaf(fmaf(-15.f, q0, span), FIFTEENTH, q0));
   if (__half_as_ushort(sh) == 0) sh = __ushort_as_half(1);
   const float zero = __half2float(zh), step = __half2float(sh);
-  const float inv = __frcp_rn(step);
-  const T2 p[4] = {a, b, c, d};
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(step));
   const uint64_t mz2 = f2_pack(-zero, -zero), inv2 = f2_pack(inv, inv);
   const uint64_t big = f2_pack(12582912.f, 12582912.f), mbig = f2_pack(-12582912.f, -12582912.f);
-  float n[8], off = 0.f;
+  // all sixteen again where t may leave [0, 15], else those near a border
+  uint32_t again = step >= 1.220703125e-4f && lo == r.x && hi == -r.y ? 0u : 0xffffu;
+  float q[4], d[16], off = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 v = Pair<T>::to_float(p[i]);
-    const uint64_t t = f2_mul(f2_add(f2_pack(v.x, v.y), mz2), inv2);
-    const uint64_t k = f2_add(f2_add(t, big), mbig);
-    float d0, d1;
-    f2_unpack(f2_sub(t, k), d0, d1);
-    f2_unpack(k, n[2 * i], n[2 * i + 1]);
-    off = fmax3(off, fabsf(d0), fabsf(d1));
-  }
-  uint32_t codes = 0;
-  if (off < 0.5f - 1.52587890625e-5f && step >= 1.220703125e-4f && lo == r.x && hi == -r.y) {
-    float q[2];
+  for (int h = 0; h < 4; ++h) {
+    float n[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      q[h] = fmaf(n[4 * h + 3], 4096.f,
-                  fmaf(n[4 * h + 2], 256.f, fmaf(n[4 * h + 1], 16.f, n[4 * h] + 8388608.f)));
-    codes = __byte_perm(__float_as_uint(q[0]), __float_as_uint(q[1]), 0x5410);
-  } else if (!nan) {
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t w = i < 2 ? x.x : i < 4 ? x.y : i < 6 ? x.z : x.w;
-      const float2 v = Pair<T>::to_float(as_pair<T2>(w));
-      codes |= kv4_code((i & 1) ? v.y : v.x, zero, step, inv) << (4 * i);
+    for (int i = 0; i < 2; ++i) {
+      const float2 v = Pair<T>::to_float(as_pair<T2>(w[2 * h + i]));
+      const uint64_t t = f2_mul(f2_add(f2_pack(v.x, v.y), mz2), inv2);
+      const uint64_t k = f2_add(f2_add(t, big), mbig);
+      float* e = d + 4 * h + 2 * i;
+      f2_unpack(f2_sub(t, k), e[0], e[1]);
+      f2_unpack(k, n[2 * i], n[2 * i + 1]);
+      off = fmax3(off, fabsf(e[0]), fabsf(e[1]));
     }
+    q[h] = fmaf(n[3], 4096.f, fmaf(n[2], 256.f, fmaf(n[1], 16.f, n[0] + 8388608.f)));
   }
-  const uint32_t params = nan ? 0x7FFF7FFFu
-                              : static_cast<uint32_t>(__half_as_ushort(sh)) |
-                                    (static_cast<uint32_t>(__half_as_ushort(zh)) << 16);
-  return make_uint2(codes, params);
+  Kv4Codes c;
+  c.lo = __byte_perm(__float_as_uint(q[0]), __float_as_uint(q[1]), 0x5410);
+  c.hi = __byte_perm(__float_as_uint(q[2]), __float_as_uint(q[3]), 0x5410);
+  c.params = nan ? 0x7FFF7FFFu
+                 : static_cast<uint32_t>(__half_as_ushort(sh)) |
+                       (static_cast<uint32_t>(__half_as_ushort(zh)) << 16);
+  constexpr float NEAR = 0.5f - 7.62939453125e-6f;
+  if (off >= NEAR) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (fabsf(d[i]) >= NEAR) again |= 1u << i;
+  }
+  if (nan || !use) c.lo = c.hi = again = 0u;
+#pragma unroll 1
+  while (again) {
+    const int i = __ffs(again) - 1;
+    again &= again - 1;
+    // selected, not indexed: the words stay in registers
+    const uint32_t p0 = (i & 2) ? w[1] : w[0], p1 = (i & 2) ? w[3] : w[2];
+    const uint32_t p2 = (i & 2) ? w[5] : w[4], p3 = (i & 2) ? w[7] : w[6];
+    const uint32_t p4 = (i & 4) ? p1 : p0, p5 = (i & 4) ? p3 : p2;
+    const float2 v = Pair<T>::to_float(as_pair<T2>((i & 8) ? p5 : p4));
+    const uint32_t code = kv4_code((i & 1) ? v.y : v.x, zero, step, inv);
+    const int at = 4 * (i & 7);
+    const uint32_t keep = ~(15u << at), put = code << at;
+    if (i < 8) c.lo = (c.lo & keep) | put; else c.hi = (c.hi & keep) | put;
+  }
+  return c;
 }
 
-// Work of append and read: LANES = d / 8 lanes take the d values of a token
-// and head, 8 each; a CTA takes 16 tokens (so that the tokens whose V codes
-// share a sector are handled together) of HEADS heads, HEADS * 16 * LANES /
-// CACHE_THREADS of them one after the other in each thread with their loads
-// under way at once.
+// Work of append and read: d / EACH lanes take the d values of a token and
+// head (EACH = 16 in the append, which divides what a vector costs by fewer
+// lanes; 8 in the read, whose lanes then store side by side); a CTA takes 16 tokens (so that the tokens whose V codes
+// share a sector are handled together) of HEADS heads, HEADS_AT_ONCE of them in
+// each thread with their loads under way together: two in the read (126 us for
+// 128K tokens, 141 us with one), one in the append, whose code then fits the
+// instruction cache (32749 tokens, read back included: 98 us with two).
 constexpr int CACHE_THREADS = 256;
-constexpr int HEADS_AT_ONCE = 2;      // vectors in flight in a thread
-template <int D>
+template <int D, int EACH, int HEADS_AT_ONCE>
 struct CacheCta {
-  static constexpr int LANES = D / 8;
+  static constexpr int LANES = D / EACH;
   static constexpr int ACROSS = CACHE_THREADS / (16 * LANES);   // heads side by side
   static constexpr int HEADS = ACROSS * HEADS_AT_ONCE;
 };
@@ -339,9 +366,8 @@ struct Place {
   long long token;
   int head0, lane;      // head u of the thread: head0 + u * ACROSS
 };
-template <int D>
+template <class C>
 __device__ __forceinline__ Place place_of(int Hkv) {
-  using C = CacheCta<D>;
   const unsigned per = (Hkv + C::HEADS - 1) / C::HEADS;
   const unsigned group = blockIdx.x / per;
   const int t = threadIdx.x;
@@ -362,20 +388,25 @@ __device__ __forceinline__ int slot_of(const Kv4CopyParams& p, long long token) 
 template <int D, class T>
 __global__ void __launch_bounds__(CACHE_THREADS) ra_kv4_append_kernel(const Kv4CopyParams p) {
   using L = Kv4<D>;
-  using C = CacheCta<D>;
+  constexpr int HEADS_AT_ONCE = 1;
+  using C = CacheCta<D, 16, HEADS_AT_ONCE>;
   constexpr int LANES = C::LANES;
-  const Place at = place_of<D>(p.Hkv);
+  const Place at = place_of<C>(p.Hkv);
   const int j = at.lane;
-  uint4 k[HEADS_AT_ONCE], v[HEADS_AT_ONCE];
+  uint4 k[HEADS_AT_ONCE][2], v[HEADS_AT_ONCE][2];
 #pragma unroll
   for (int u = 0; u < HEADS_AT_ONCE; ++u) {
     const int head = at.head0 + u * C::ACROSS;
-    k[u] = v[u] = make_uint4(0, 0, 0, 0);
-    if (at.token < p.T && head < p.Hkv) {
-      k[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.k) + at.token * p.k_stride +
-                                             head * D + j * 8);
-      v[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + at.token * p.v_stride +
-                                             head * D + j * 8);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      k[u][e] = v[u][e] = make_uint4(0, 0, 0, 0);
+      if (at.token < p.T && head < p.Hkv) {
+        const int o = head * D + j * 16 + e * 8;
+        k[u][e] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.k) +
+                                                  at.token * p.k_stride + o);
+        v[u][e] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) +
+                                                  at.token * p.v_stride + o);
+      }
     }
   }
   const int slot = slot_of(p, at.token);
@@ -389,27 +420,31 @@ __global__ void __launch_bounds__(CACHE_THREADS) ra_kv4_append_kernel(const Kv4C
 #pragma unroll
   for (int u = 0; u < HEADS_AT_ONCE; ++u) {
     const int head = at.head0 + u * C::ACROSS;
-    const uint2 kc = kv4_encode8<T, LANES>(k[u]);
-    const uint2 vc = kv4_encode8<T, LANES>(v[u]);
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, vc.x, LANES);
-    if (slot < 0 || head >= p.Hkv) continue;
+    const bool use = slot >= 0 && head < p.Hkv;
+    const Kv4Codes kc = kv4_encode16<T, LANES>(k[u][0], k[u][1], use);
+    const Kv4Codes vc = kv4_encode16<T, LANES>(v[u][0], v[u][1], use);
+    const uint32_t send = side == 0 ? vc.hi : vc.lo;
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, send, LANES);
+    if (!use) continue;
     uint8_t* blk = p.cache + ((static_cast<long long>(page) * p.Hkv + head) * (p.page >> 4) +
                               (o >> 4)) * L::BLOCK_BYTES;
-    *reinterpret_cast<uint32_t*>(blk + i * L::ROW + j * 4) = kc.x;
+    *reinterpret_cast<uint2*>(blk + i * L::ROW + j * 8) = make_uint2(kc.lo, kc.hi);
     uint8_t* vb = blk + L::OFF_V;
     if (paired) {
-      // both tokens of a word in this warp: each lane stores one whole word
-      const uint32_t word = side == 0 ? __byte_perm(vc.x, other, 0x5410)
-                                      : __byte_perm(vc.x, other, 0x3276);
-      *reinterpret_cast<uint32_t*>(vb + L::v_code_offset(i & ~1, 2 * j + side)) = word;
+      // both tokens of a word in this warp: the even one's lane stores the
+      // words of its first eight elements, the odd one's those of the others
+      const uint32_t even = side == 0 ? vc.lo : got, odd = side == 0 ? got : vc.hi;
+      *reinterpret_cast<uint2*>(vb + L::v_code_offset(i & ~1, 4 * j + 2 * side)) =
+          make_uint2(__byte_perm(even, odd, 0x5410), __byte_perm(even, odd, 0x7632));
     } else {
-      *reinterpret_cast<uint16_t*>(vb + L::v_code_offset(i, 2 * j)) = static_cast<uint16_t>(vc.x);
-      *reinterpret_cast<uint16_t*>(vb + L::v_code_offset(i, 2 * j + 1)) =
-          static_cast<uint16_t>(vc.x >> 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<uint16_t*>(vb + L::v_code_offset(i, 4 * j + e)) =
+            static_cast<uint16_t>((e < 2 ? vc.lo : vc.hi) >> (16 * (e & 1)));
     }
     if (j == 0) {
-      *reinterpret_cast<uint32_t*>(blk + L::OFF_KP + 4 * i) = kc.y;
-      *reinterpret_cast<uint32_t*>(blk + L::OFF_VP + 4 * i) = vc.y;
+      *reinterpret_cast<uint32_t*>(blk + L::OFF_KP + 4 * i) = kc.params;
+      *reinterpret_cast<uint32_t*>(blk + L::OFF_VP + 4 * i) = vc.params;
     }
   }
 }
@@ -458,8 +493,9 @@ __device__ __forceinline__ void decode8(T* dst, uint32_t codes, uint32_t params)
 template <int D, class T>
 __global__ void __launch_bounds__(CACHE_THREADS) ra_kv4_read_kernel(const Kv4CopyParams p) {
   using L = Kv4<D>;
-  using C = CacheCta<D>;
-  const Place at = place_of<D>(p.Hkv);
+  constexpr int HEADS_AT_ONCE = 2;
+  using C = CacheCta<D, 8, HEADS_AT_ONCE>;
+  const Place at = place_of<C>(p.Hkv);
   const int j = at.lane;
   if (at.token >= p.T) return;
   const int slot = slot_of(p, at.token);
@@ -474,13 +510,11 @@ __global__ void __launch_bounds__(CACHE_THREADS) ra_kv4_read_kernel(const Kv4Cop
       const uint8_t* blk = p.cache + ((static_cast<long long>(page) * p.Hkv + head) *
                                           (p.page >> 4) + (o >> 4)) * L::BLOCK_BYTES;
       kc[u] = *reinterpret_cast<const uint32_t*>(blk + i * L::ROW + j * 4);
-      const uint8_t* vb = blk + L::OFF_V;
-      // the words with the token's halves of elements 8 j .. 8 j + 7, side by
-      // side with those of its neighbour's
-      const uint32_t w0 = *reinterpret_cast<const uint32_t*>(vb + L::v_code_offset(i & ~1, 2 * j));
-      const uint32_t w1 =
-          *reinterpret_cast<const uint32_t*>(vb + L::v_code_offset(i & ~1, 2 * j + 1));
-      vc[u] = __byte_perm(w0, w1, (i & 1) ? 0x7632 : 0x5410);
+      // the words with the token's halves of its elements, side by side with
+      // those of its neighbour's
+      const uint2 w = *reinterpret_cast<const uint2*>(blk + L::OFF_V +
+                                                      L::v_code_offset(i & ~1, 2 * j));
+      vc[u] = __byte_perm(w.x, w.y, (i & 1) ? 0x7632 : 0x5410);
       kp[u] = *reinterpret_cast<const uint32_t*>(blk + L::OFF_KP + 4 * i);
       vp[u] = *reinterpret_cast<const uint32_t*>(blk + L::OFF_VP + 4 * i);
     }
@@ -495,11 +529,11 @@ __global__ void __launch_bounds__(CACHE_THREADS) ra_kv4_read_kernel(const Kv4Cop
   }
 }
 
-template <int D>
+template <class C>
 cudaError_t launch_copy(void (*kernel)(const Kv4CopyParams), const Kv4CopyParams& p,
                         cudaStream_t stream) {
   const long long groups = (p.T + 15) / 16;
-  const long long grid = groups * ((p.Hkv + CacheCta<D>::HEADS - 1) / CacheCta<D>::HEADS);
+  const long long grid = groups * ((p.Hkv + C::HEADS - 1) / C::HEADS);
   if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   kernel<<<static_cast<unsigned>(grid), CACHE_THREADS, 0, stream>>>(p);
   return cudaGetLastError();
@@ -537,21 +571,21 @@ cudaError_t launch_kv4_plan(const Kv4PlanParams& p, cudaStream_t stream) {
 
 cudaError_t launch_kv4_append(const Kv4CopyParams& p, int d, int dtype, cudaStream_t stream) {
   if (dtype == RA_BF16)
-    return d == 128 ? launch_copy<128>(ra_kv4_append_kernel<128, __nv_bfloat16>, p, stream)
-                    : launch_copy<64>(ra_kv4_append_kernel<64, __nv_bfloat16>, p, stream);
-  return d == 128 ? launch_copy<128>(ra_kv4_append_kernel<128, __half>, p, stream)
-                  : launch_copy<64>(ra_kv4_append_kernel<64, __half>, p, stream);
+    return d == 128 ? launch_copy<CacheCta<128, 16, 1>>(ra_kv4_append_kernel<128, __nv_bfloat16>, p, stream)
+                    : launch_copy<CacheCta<64, 16, 1>>(ra_kv4_append_kernel<64, __nv_bfloat16>, p, stream);
+  return d == 128 ? launch_copy<CacheCta<128, 16, 1>>(ra_kv4_append_kernel<128, __half>, p, stream)
+                  : launch_copy<CacheCta<64, 16, 1>>(ra_kv4_append_kernel<64, __half>, p, stream);
 }
 
 cudaError_t launch_kv4_read(const Kv4CopyParams& p, int d, int dtype, cudaStream_t stream) {
   if (dtype == RA_BF16)
-    return d == 128 ? launch_copy<128>(ra_kv4_read_kernel<128, __nv_bfloat16>, p, stream)
-                    : launch_copy<64>(ra_kv4_read_kernel<64, __nv_bfloat16>, p, stream);
+    return d == 128 ? launch_copy<CacheCta<128, 8, 2>>(ra_kv4_read_kernel<128, __nv_bfloat16>, p, stream)
+                    : launch_copy<CacheCta<64, 8, 2>>(ra_kv4_read_kernel<64, __nv_bfloat16>, p, stream);
   if (dtype == RA_FP16)
-    return d == 128 ? launch_copy<128>(ra_kv4_read_kernel<128, __half>, p, stream)
-                    : launch_copy<64>(ra_kv4_read_kernel<64, __half>, p, stream);
-  return d == 128 ? launch_copy<128>(ra_kv4_read_kernel<128, float>, p, stream)
-                  : launch_copy<64>(ra_kv4_read_kernel<64, float>, p, stream);
+    return d == 128 ? launch_copy<CacheCta<128, 8, 2>>(ra_kv4_read_kernel<128, __half>, p, stream)
+                    : launch_copy<CacheCta<64, 8, 2>>(ra_kv4_read_kernel<64, __half>, p, stream);
+  return d == 128 ? launch_copy<CacheCta<128, 8, 2>>(ra_kv4_read_kernel<128, float>, p, stream)
+                  : launch_copy<CacheCta<64, 8, 2>>(ra_kv4_read_kernel<64, float>, p, stream);
 }
 
 cudaError_t read_and_clear_kv4_cache_status(unsigned long long* out) {
