@@ -64,15 +64,11 @@ namespace kv4d {
 #ifndef KV4_UC
 #define KV4_UC 8
 #endif
-#ifndef KV4_STAGES
-#define KV4_STAGES 2
-#endif
 #ifndef KV4_WARPS
 #define KV4_WARPS 8
 #endif
 constexpr int WARPS = KV4_WARPS;
 constexpr int THREADS = WARPS * 32;
-constexpr int STAGES = KV4_STAGES;          // of two blocks each
 constexpr int MIN_CELLS = KV4_MINC;      // cells below which a stretch is not cut further
 // What a unit costs a warp beside its blocks (start, store), in blocks: it
 // takes so many cells of the line before its first block.
@@ -87,6 +83,8 @@ __device__ unsigned long long g_status = 0ull;
 // the warp has read its last block; the head pieces; their m and l; barriers.
 template <int D, int NT>
 struct Smem {
+  static constexpr int STAGES = 2;   // of two blocks each
+  static constexpr int CTAS = D * NT <= 128 ? 16 / WARPS : 8 / WARPS;   // on an SM
   static constexpr int WRING = STAGES * 2 * Kv4<D>::BLOCK_BYTES;
   static constexpr int ROWS = 8 * NT;
   static constexpr int RS = D + 4;                       // row stride of a piece
@@ -223,12 +221,12 @@ __device__ __forceinline__ bool kv4_last(unsigned* counter, int n, int* s_last) 
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(THREADS, (NT == 1 ? 16 : 8) / WARPS)
+__global__ void __launch_bounds__(THREADS, (Smem<D, NT>::CTAS))
     ra_kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p) {
   using L = Kv4<D>;
   using S = Smem<D, NT>;
   constexpr int WPL = D / 32;        // code words of a row per lane (16 or 8 bytes)
-  constexpr int ROWS = 8 * NT;
+  constexpr int ROWS = 8 * NT, STAGES = S::STAGES;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t s_abort;
   __shared__ int s_last;
@@ -692,7 +690,7 @@ cudaError_t launch(Kv4AttnParams p, int num_sms, int max_ctas, cudaStream_t stre
     if (e != cudaSuccess) return e;
     configured_dev[dev] = 1;
   }
-  int grid = num_sms * ((NT == 1 ? 16 : 8) / WARPS);
+  int grid = num_sms * S::CTAS;
   if (max_ctas > 0 && max_ctas < grid) grid = max_ctas;
   if (grid > KV4_MAX_CTAS) grid = KV4_MAX_CTAS;
   // no more units, and with the longest requests the table can name cells,
