@@ -79,6 +79,13 @@ def load(path: str = LIB_PATH):
     return _lib
 
 
+def function(name: str):
+    """The library's function `name` itself, for calls whose cost counts in
+    microseconds: the caller converts nothing and passes a non-zero result to
+    ``_check``."""
+    return getattr(load(), name)
+
+
 def status_string(status: int) -> str:
     return load().ring_attn_status_string(status).decode()
 

@@ -319,34 +319,23 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-class _Here:
-    """``_on`` where nothing has to be switched: the tensors' device is the
-    current one and the call uses its current stream."""
-
-    __slots__ = ("handle",)
-
-    def __init__(self, handle):
-        self.handle = handle
-
-    def __enter__(self):
-        return self.handle
-
-    def __exit__(self, *exc):
-        return False
+_bf16, _f16, _f32, _i32, _u8 = (torch.bfloat16, torch.float16, torch.float32, torch.int32,
+                                torch.uint8)
+_native = {}
 
 
-def _here(device, stream):
-    index = device.index
-    if stream is None and _current_device() == index:
-        return _Here(_raw_stream(index))
-    return _on(device, stream)
+def _fn(name: str):
+    f = _native.get(name)
+    if f is None:
+        f = _native[name] = _lib.function(name)
+    return f
 
 
-def _is(t, dtype, ndim: int, device) -> bool:
-    """Whether t is a contiguous tensor of that type and rank on `device`
-    (one expression: these calls are counted in microseconds)."""
+def _is(t, dtype, ndim: int, index: int) -> bool:
+    """Whether t is a contiguous tensor of that type and rank on CUDA device
+    `index` (one expression: these calls are counted in microseconds)."""
     return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim
-            and t.device == device and t.is_contiguous())
+            and t.get_device() == index and t.is_contiguous())
 
 
 def _check_same_device(device, **tensors):
@@ -357,35 +346,39 @@ def _check_same_device(device, **tensors):
 
 def _check_rows(t: torch.Tensor, name: str):
     """[T, H, d] whose tokens may be strided (a slice of a fused projection),
-    each token's [H, d] contiguous.  Returns the token stride in elements."""
+    each token's [H, d] contiguous.  Returns T, H, d and the token stride in
+    elements."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16 and t.dtype != torch.float16:
+    if t.dtype is not _bf16 and t.dtype is not _f16:
         raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name} must be a 3-d tensor [T, H, d]")
     T, H, d = t.shape
+    if t.is_contiguous():
+        return T, H, d, H * d
     st = t.stride()
-    if T == 0 or t.is_contiguous():
-        return H * d
+    if T == 0:
+        return T, H, d, H * d
     if (d > 1 and st[2] != 1) or (H > 1 and st[1] != d):
         raise ValueError(f"each token's [H, d] of {name} must be contiguous")
     if T == 1:
-        return H * d
+        return T, H, d, H * d
     if st[0] < H * d:
         raise ValueError(f"the tokens of {name} must not overlap (stride {st[0]})")
-    return st[0]
+    return T, H, d, st[0]
 
 
 def _cache_shape(cache: torch.Tensor):
     """(num_pages, Hkv, page, d) of a cache tensor."""
-    _check_cuda(cache, "cache", torch.uint8, 4)
+    if not (isinstance(cache, torch.Tensor) and cache.is_cuda and cache.dtype is _u8
+            and cache.dim() == 4 and cache.is_contiguous()):
+        _check_cuda(cache, "cache", _u8, 4)
     P, Hkv, blocks, nbytes = cache.shape
-    d = nbytes // 16 - 8
-    if nbytes != 16 * (d + 8) or d not in (64, 128) or blocks < 1 or Hkv < 1:
+    if (nbytes != 2176 and nbytes != 1152) or blocks < 1 or Hkv < 1:
         raise ValueError(f"cache must be [num_pages, Hkv, page / 16, 16 * (d + 8)] with d 64 or "
                          f"128, got {tuple(cache.shape)}")
-    return P, Hkv, 16 * blocks, d
+    return P, Hkv, 16 * blocks, 128 if nbytes == 2176 else 64
 
 
 def kv4_cache(num_pages: int, Hkv: int, d: int, page: int = 64, device="cuda") -> torch.Tensor:
@@ -420,13 +413,14 @@ def kv4_plan(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, pool: t
     that do not fit), in which case nothing changes.  ``out``: tensors of
     these shapes for the results; the first three may be the inputs
     themselves."""
-    i32 = torch.int32
-    _check_cuda(table, "table", i32, 2)
-    dev = table.device
-    if not (_is(lens, i32, 1, dev) and _is(add, i32, 1, dev) and _is(pool, i32, 1, dev)):
+    if not (isinstance(table, torch.Tensor) and table.is_cuda and table.dtype is _i32
+            and table.dim() == 2 and table.is_contiguous()):
+        _check_cuda(table, "table", _i32, 2)
+    index = table.get_device()
+    if not (_is(lens, _i32, 1, index) and _is(add, _i32, 1, index) and _is(pool, _i32, 1, index)):
         for t, n in ((lens, "lens"), (add, "add"), (pool, "pool")):
-            _check_cuda(t, n, i32, 1)
-        _check_same_device(dev, lens=lens, add=add, pool=pool)
+            _check_cuda(t, n, _i32, 1)
+        _check_same_device(table.device, lens=lens, add=add, pool=pool)
     R, W = table.shape
     if lens.shape[0] != R or add.shape[0] != R:
         raise ValueError(f"lens {tuple(lens.shape)}, add {tuple(add.shape)} and table "
@@ -436,21 +430,33 @@ def kv4_plan(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, pool: t
         raise ValueError("pool must be [num_pages + 1]")
     if max_tokens < 0:
         raise ValueError(f"max_tokens must be >= 0, got {max_tokens}")
-    with _here(dev, stream) as sh:
-        if out is None:
-            out = [torch.empty(shape, dtype=i32, device=dev)
-                   for shape in (R, (R, W), num_pages + 1, R + 1, max_tokens, 1)]
-        else:
-            for t, n, shape in zip(out, ("lens", "table", "pool", "cu", "slots", "shortage"),
-                                   ((R,), (R, W), (num_pages + 1,), (R + 1,), (max_tokens,), (1,)),
-                                   strict=True):
-                _check_out(t, "out " + n, torch.int32, shape)
-                _check_same_device(dev, **{"out_" + n: t})
-        lo, to, po, cu, slots, shortage = out
-        _lib.ring_attn_kv4_plan(lens.data_ptr(), add.data_ptr(), table.data_ptr(), pool.data_ptr(),
-                                lo.data_ptr(), to.data_ptr(), po.data_ptr(), cu.data_ptr(),
-                                slots.data_ptr(), shortage.data_ptr(), R, W, num_pages, page,
-                                max_tokens, sh)
+    if stream is not None or _current_device() != index:
+        with _on(table.device, stream) as sh:
+            return _plan(lens, add, table, pool, page, max_tokens, out, index, R, W, num_pages, sh)
+    return _plan(lens, add, table, pool, page, max_tokens, out, index, R, W, num_pages,
+                 _raw_stream(index))
+
+
+def _plan(lens, add, table, pool, page, max_tokens, out, index, R, W, num_pages, sh):
+    if out is None:
+        new, dev = torch.empty, table.device
+        out = (new(R, dtype=_i32, device=dev), new((R, W), dtype=_i32, device=dev),
+               new(num_pages + 1, dtype=_i32, device=dev), new(R + 1, dtype=_i32, device=dev),
+               new(max_tokens, dtype=_i32, device=dev), new(1, dtype=_i32, device=dev))
+    else:
+        for t, n, shape in zip(out, ("lens", "table", "pool", "cu", "slots", "shortage"),
+                               ((R,), (R, W), (num_pages + 1,), (R + 1,), (max_tokens,), (1,)),
+                               strict=True):
+            if not (_is(t, _i32, len(shape), index) and t.shape == shape):
+                _check_out(t, "out " + n, _i32, shape)
+                _check_same_device(table.device, **{"out_" + n: t})
+    lo, to, po, cu, slots, shortage = out
+    st = _fn("ring_attn_kv4_plan")(
+        lens.data_ptr(), add.data_ptr(), table.data_ptr(), pool.data_ptr(), lo.data_ptr(),
+        to.data_ptr(), po.data_ptr(), cu.data_ptr(), slots.data_ptr(), shortage.data_ptr(), R, W,
+        num_pages, page, max_tokens, sh)
+    if st:
+        _lib._check(st)
     return lo, to, po, cu, slots, shortage
 
 
@@ -458,21 +464,30 @@ def kv4_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: tor
                stream=None):
     """Quantise k, v [T, Hkv, d] (bf16 or fp16; tokens may be strided) into
     the cache at ``slots`` (int32 [T], distinct; -1 skips a token)."""
-    ks, vs = _check_rows(k, "k"), _check_rows(v, "v")
+    T, H, dk, ks = _check_rows(k, "k")
+    Tv, Hv, dv, vs = _check_rows(v, "v")
     P, Hkv, page, d = _cache_shape(cache)
-    T = k.shape[0]
-    if k.shape != (T, Hkv, d) or v.shape != k.shape or k.dtype != v.dtype:
+    if not (T == Tv and H == Hv == Hkv and dk == dv == d and k.dtype is v.dtype):
         raise ValueError(f"k {tuple(k.shape)} {k.dtype} and v {tuple(v.shape)} {v.dtype} must be "
                          f"[T, {Hkv}, {d}] of one type")
-    dev = cache.device
-    if not (_is(slots, torch.int32, 1, dev) and slots.shape[0] == T and k.device == dev
-            and v.device == dev):
-        _check_out(slots, "slots", torch.int32, (T,))
-        _check_same_device(dev, k=k, v=v, slots=slots)
-    with _here(dev, stream) as sh:
-        _lib.ring_attn_kv4_append(k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(),
-                                  cache.data_ptr(), T, Hkv, d, _CODE[k.dtype], P, page, sh)
+    index = cache.get_device()
+    if not (_is(slots, _i32, 1, index) and slots.shape[0] == T and k.get_device() == index
+            and v.get_device() == index):
+        _check_out(slots, "slots", _i32, (T,))
+        _check_same_device(cache.device, k=k, v=v, slots=slots)
+    if stream is not None or _current_device() != index:
+        with _on(cache.device, stream) as sh:
+            _append(k, ks, v, vs, slots, cache, T, Hkv, d, P, page, sh)
+    else:
+        _append(k, ks, v, vs, slots, cache, T, Hkv, d, P, page, _raw_stream(index))
     return cache
+
+
+def _append(k, ks, v, vs, slots, cache, T, Hkv, d, P, page, sh):
+    st = _fn("ring_attn_kv4_append")(k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(),
+                                     cache.data_ptr(), T, Hkv, d, _CODE[k.dtype], P, page, sh)
+    if st:
+        _lib._check(st)
 
 
 def kv4_read(cache: torch.Tensor, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
@@ -480,26 +495,35 @@ def kv4_read(cache: torch.Tensor, slots: torch.Tensor, dtype: torch.dtype = torc
     """The cached keys and values at ``slots`` (int32 [T]; zeros for -1):
     (k, v) of ``dtype`` (bf16, fp16 or fp32), [T, Hkv, d]."""
     P, Hkv, page, d = _cache_shape(cache)
-    dev = cache.device
-    if not _is(slots, torch.int32, 1, dev):
-        _check_cuda(slots, "slots", torch.int32, 1)
-        _check_same_device(dev, slots=slots)
+    index = cache.get_device()
+    if not _is(slots, _i32, 1, index):
+        _check_cuda(slots, "slots", _i32, 1)
+        _check_same_device(cache.device, slots=slots)
     if dtype not in _CODE:
         raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
-    T = slots.shape[0]
-    with _here(dev, stream) as sh:
-        if k is None:
-            k = torch.empty((T, Hkv, d), dtype=dtype, device=dev)
-        elif not (_is(k, dtype, 3, dev) and k.shape == (T, Hkv, d)):
-            _check_out(k, "k", dtype, (T, Hkv, d))
-            _check_same_device(dev, k=k)
-        if v is None:
-            v = torch.empty((T, Hkv, d), dtype=dtype, device=dev)
-        elif not (_is(v, dtype, 3, dev) and v.shape == (T, Hkv, d)):
-            _check_out(v, "v", dtype, (T, Hkv, d))
-            _check_same_device(dev, v=v)
-        _lib.ring_attn_kv4_read(cache.data_ptr(), slots.data_ptr(), k.data_ptr(), v.data_ptr(), T,
-                                Hkv, d, _CODE[dtype], P, page, sh)
+    if stream is not None or _current_device() != index:
+        with _on(cache.device, stream) as sh:
+            return _read(cache, slots, dtype, k, v, index, P, Hkv, page, d, sh)
+    return _read(cache, slots, dtype, k, v, index, P, Hkv, page, d, _raw_stream(index))
+
+
+def _read(cache, slots, dtype, k, v, index, P, Hkv, page, d, sh):
+    T, dev = slots.shape[0], cache.device
+    shape = (T, Hkv, d)
+    if k is None:
+        k = torch.empty(shape, dtype=dtype, device=dev)
+    elif not (_is(k, dtype, 3, index) and k.shape == shape):
+        _check_out(k, "k", dtype, shape)
+        _check_same_device(dev, k=k)
+    if v is None:
+        v = torch.empty(shape, dtype=dtype, device=dev)
+    elif not (_is(v, dtype, 3, index) and v.shape == shape):
+        _check_out(v, "v", dtype, shape)
+        _check_same_device(dev, v=v)
+    st = _fn("ring_attn_kv4_read")(cache.data_ptr(), slots.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                   T, Hkv, d, _CODE[dtype], P, page, sh)
+    if st:
+        _lib._check(st)
     return k, v
 
 
@@ -526,53 +550,63 @@ def kv4_fwd(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens: tor
     ``out_dtype`` float32, lse fp32 [T, Hq]); rows from cu[R] on are not
     written.  ``max_q`` bounds the query tokens of a request (default T).
     ``workspace`` (``kv4_workspace``) is allocated and zeroed if omitted."""
-    qs = _check_rows(q, "q")
+    T, Hq, dq, qs = _check_rows(q, "q")
     P, Hkv, page, d = _cache_shape(cache)
-    T, Hq, dq = q.shape
     if dq != d or Hq % Hkv != 0 or Hq < 1:
         raise ValueError(f"q {tuple(q.shape)} does not match a cache of {Hkv} heads of {d}")
-    i32, dev = torch.int32, q.device
-    if not (_is(table, i32, 2, dev) and _is(lens, i32, 1, dev) and cache.device == dev):
-        _check_cuda(table, "table", i32, 2)
-        _check_cuda(lens, "lens", i32, 1)
-        _check_same_device(dev, cache=cache, table=table, lens=lens)
+    index = q.get_device()
+    if not (_is(table, _i32, 2, index) and _is(lens, _i32, 1, index)
+            and cache.get_device() == index):
+        _check_cuda(table, "table", _i32, 2)
+        _check_cuda(lens, "lens", _i32, 1)
+        _check_same_device(q.device, cache=cache, table=table, lens=lens)
     R, W = table.shape
     if lens.shape[0] != R:
         raise ValueError(f"lens {tuple(lens.shape)} does not match table {tuple(table.shape)}")
     if cu is not None:
-        if not (_is(cu, i32, 1, dev) and cu.shape[0] == R + 1):
-            _check_out(cu, "cu", i32, (R + 1,))
-            _check_same_device(dev, cu=cu)
+        if not (_is(cu, _i32, 1, index) and cu.shape[0] == R + 1):
+            _check_out(cu, "cu", _i32, (R + 1,))
+            _check_same_device(q.device, cu=cu)
     elif T != R:
         raise ValueError(f"without cu every request has one query token, got {T} for {R} requests")
-    if max_q is None:
-        max_q = T
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
     if out_dtype is None:
         out_dtype = q.dtype if out is None else out.dtype
-    if out_dtype is not q.dtype and out_dtype is not torch.float32:
+    if out_dtype is not q.dtype and out_dtype is not _f32:
         raise TypeError(f"the output is {q.dtype} or float32, got {out_dtype}")
-    with _here(dev, stream) as sh:
-        if out is None:
-            out = torch.empty((T, Hq, d), dtype=out_dtype, device=dev)
-        elif not (_is(out, out_dtype, 3, dev) and out.shape == (T, Hq, d)):
-            _check_out(out, "out", out_dtype, (T, Hq, d))
-            _check_same_device(dev, out=out)
-        if lse is None:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-        elif not (_is(lse, torch.float32, 2, dev) and lse.shape == (T, Hq)):
-            _check_out(lse, "lse", torch.float32, (T, Hq))
-            _check_same_device(dev, lse=lse)
-        if workspace is None:
-            workspace = kv4_workspace(dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-        _lib.ring_attn_kv4_fwd(q.data_ptr(), qs, cache.data_ptr(), table.data_ptr(),
-                               lens.data_ptr(), 0 if cu is None else cu.data_ptr(), out.data_ptr(),
-                               lse.data_ptr(), T, R, Hq, Hkv, d, W, P, page, max_q, causal, scale,
-                               _CODE[q.dtype], _CODE[out_dtype], workspace.data_ptr(),
-                               workspace.numel() * workspace.element_size(), sh)
+    shape = (P, Hkv, page, d, T, Hq, qs, R, W, T if max_q is None else max_q, causal,
+             1.0 / math.sqrt(d) if scale is None else scale)
+    if stream is not None or _current_device() != index:
+        with _on(q.device, stream) as sh:
+            return _cache_fwd(q, cache, table, lens, cu, out, lse, out_dtype, workspace, index,
+                              shape, sh)
+    return _cache_fwd(q, cache, table, lens, cu, out, lse, out_dtype, workspace, index, shape,
+                      _raw_stream(index))
+
+
+def _cache_fwd(q, cache, table, lens, cu, out, lse, out_dtype, workspace, index, shape, sh):
+    P, Hkv, page, d, T, Hq, qs, R, W, max_q, causal, scale = shape
+    dev = q.device
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=out_dtype, device=dev)
+    elif not (_is(out, out_dtype, 3, index) and out.shape == (T, Hq, d)):
+        _check_out(out, "out", out_dtype, (T, Hq, d))
+        _check_same_device(dev, out=out)
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=_f32, device=dev)
+    elif not (_is(lse, _f32, 2, index) and lse.shape == (T, Hq)):
+        _check_out(lse, "lse", _f32, (T, Hq))
+        _check_same_device(dev, lse=lse)
+    if workspace is None:
+        workspace = kv4_workspace(dev)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    st = _fn("ring_attn_kv4_fwd")(
+        q.data_ptr(), qs, cache.data_ptr(), table.data_ptr(), lens.data_ptr(),
+        0 if cu is None else cu.data_ptr(), out.data_ptr(), lse.data_ptr(), T, R, Hq, Hkv, d, W, P,
+        page, max_q, bool(causal), scale, _CODE[q.dtype], _CODE[out_dtype], workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), sh)
+    if st:
+        _lib._check(st)
     return out, lse
 
 
