@@ -6,9 +6,9 @@
 //   query heads, packed token-major; a unit is 256 of them (two tiles of 128)
 //   over the tokens they see.  One CTA per SM; the roles and the order of the
 //   MMAs are the bf16 forward's (ra_fwd_roles.cuh).
-// * Warps 0-3 and 4-7 own a row tile each, one row a thread: they bring the
-//   row's q into shared memory (fp16, scaled by a power of two, exact), read S
-//   from tensor memory, form s = ks C + kz sum(q) in fp32 (C = q . codes; the steps
+// * Warps 0-3 and 4-7 own a row tile each: they bring their rows' q into
+//   shared memory (fp16, scaled by a power of two, exact), read S from tensor
+//   memory, form s = ks C + kz sum(q) in fp32 (C = q . codes; the steps
 //   and zeros lie in shared memory), keep the running maximum and sum, and
 //   write P in fp16 over S.
 // * Warp 8 copies the blocks' K and V parts into a ring of raw stages; warps
@@ -64,7 +64,8 @@ constexpr int UNIT_COST = 2;  // what a unit costs beside its tiles, in tiles
 constexpr int MIN_TILES = 8;  // tiles below which a stretch is not cut further
 constexpr int FOLD = 16;      // pieces that one CTA folds at a time
 constexpr float P_SHIFT = 5.f;         // p = 2^P_SHIFT at the reference
-constexpr float P_LIMIT_LOG2 = 15.f;   // beyond which the reference moves
+constexpr float P_LIMIT = 32768.f;     // beyond which the reference moves
+constexpr float Q_SCALE = 256.f;       // of q in fp16, see Rows
 
 __device__ unsigned long long g_status = 0ull;
 
@@ -428,67 +429,64 @@ __device__ void unpack_role(const Kv4AttnParams& p, const Bars& br, uint32_t bas
         const uint32_t have = held[rs];
         const int room = len - (t0 + t) * TILE_KEYS;   // tokens of the tile
         if (v == 0) {
-          // K: 16 bytes are 32 codes of one token, four swizzle chunks
-          constexpr int CPR = D / 32;                    // 16-byte chunks of a row
+          // K: 16 bytes are 32 codes of one token, four swizzle chunks; the
+          // eight lanes of a phase take eight tokens, whose chunks then lie in
+          // eight places
+          constexpr int CPR = D / 32;                    // 16-byte parts of a row
 #pragma unroll 1
-          for (int c = 0; c < CPR; ++c) {
-            const int id = i + 128 * c, key = id / CPR, q = id % CPR;
+          for (int q = 0; q < CPR; ++q) {
             uint32_t x[4];
-            lds128(x, raw + (key >> 4) * C::PART + (key & 15) * (D / 2) + q * 16);
-            const uint32_t row = dst + (q >> 1) * BOX_BYTES + key * 128;
+            lds128(x, raw + (i >> 4) * C::PART + (i & 15) * (D / 2) + q * 16);
+            const uint32_t row = dst + (q >> 1) * BOX_BYTES + i * 128;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              // odd boxes in another order: the eight lanes of a phase then
-              // store to eight different chunks
-              const int ww = w ^ ((q >> 1) << 1);
-              const uint32_t a = ww == 0 ? x[0] : ww == 1 ? x[1] : ww == 2 ? x[2] : x[3];
-              const uint32_t b = a >> 8;
-              const int chunk = ((q & 1) * 4 + ww) ^ (key & 7);
-              sts128(row + chunk * 16, a & 0x000f000fu, a & 0x00f000f0u, b & 0x000f000fu,
-                     b & 0x00f000f0u);
+              const uint32_t y = x[w] >> 8;
+              sts128(row + (((q & 1) * 4 + w) ^ (i & 7)) * 16, x[w] & 0x000f000fu,
+                     x[w] & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u);
             }
           }
-          // steps and zeros of the tile's tokens
+          // step and zero of token i: pairs of tokens as (step, step, zero, zero)
           const uint32_t w =
               lds32(raw + (i >> 4) * C::PART + KV4_BLOCK * (D / 2) + (i & 15) * 4);
           const float2 sz = ((have >> (i >> 4)) & 1u) ? kv4_params(w) : make_float2(0.f, 0.f);
-          const uint32_t par = base + C::OFF_PAR + (tile % NPAR) * TILE_KEYS * 8 + i * 4;
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(par), "f"(sz.x) : "memory");
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(par + TILE_KEYS * 4), "f"(sz.y) : "memory");
+          const uint32_t par =
+              base + C::OFF_PAR + (tile % NPAR) * TILE_KEYS * 8 + (i >> 1) * 16 + (i & 1) * 4;
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(par),
+                       "f"(sz.x * (p.scale_log2 * (16777216.f / Q_SCALE))) : "memory");
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(par + 8), "f"(sz.y * p.scale_log2) : "memory");
           if (i == 0) held[NRAW + tile % NPAR] = have;
           mbar_arrive(br.par_full(tile % NPAR));
         } else {
-          // V: D / 8 bytes of a lane are D / 8 values of two tokens
-          constexpr int WPL = D / 32;                    // words of a lane
+          // V: thread i has two tokens, ka and ka + 1, and every second group
+          // of D / 8 elements; their codes lie side by side in the block
+          constexpr int WPL = D / 32;                    // words of a group
+          const int kp = i & 63, blk = kp >> 3;
+          const int ka = 2 * kp;
+          const uint32_t part = raw + blk * C::PART;
+          uint32_t wa = lds32(part + KV4_BLOCK * (D / 2) + (ka & 15) * 4);
+          uint32_t wb = lds32(part + KV4_BLOCK * (D / 2) + (ka & 15) * 4 + 4);
+          const bool in = (have >> blk) & 1u;
+          // tokens that are not there: zeros, whatever the stage holds
+          if (!in || ka >= room) wa = 0u;
+          if (!in || ka + 1 >= room) wb = 0u;
+          if ((wa & 0x7fffu) > 0x7c00u) {
+            atomicMin(&pieces[u].nan_at, (t0 + t) * TILE_KEYS + ka);
+            wa = 0u;
+          }
+          if ((wb & 0x7fffu) > 0x7c00u) {
+            atomicMin(&pieces[u].nan_at, (t0 + t) * TILE_KEYS + ka + 1);
+            wb = 0u;
+          }
+          const uint32_t step = __byte_perm(wa, wb, 0x5410), zero = __byte_perm(wa, wb, 0x7632);
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            const int id = i + 128 * c;                  // [block][half][lane]
-            const int blk = id >> 6, half = (id >> 5) & 1, ln = id & 31;
-            const int g = ln >> 2, tt = ln & 3;
-            const int ka = blk * 16 + half * 8 + 2 * tt;   // tokens ka, ka + 1
-            const uint32_t part = raw + blk * C::PART;
+          for (int g = i >> 6; g < 8; g += 2) {
             uint32_t x[WPL];
-            const uint32_t src = part + half * (4 * D) + ln * (4 * WPL);
+            const uint32_t src = part + ((kp >> 2) & 1) * (4 * D) + (g * 4 + (kp & 3)) * (4 * WPL);
             if constexpr (WPL == 4) {
               lds128(x, src);
             } else {
               asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(src));
             }
-            uint32_t wa = lds32(part + KV4_BLOCK * (D / 2) + (ka & 15) * 4);
-            uint32_t wb = lds32(part + KV4_BLOCK * (D / 2) + (ka & 15) * 4 + 4);
-            const bool in = (have >> blk) & 1u;
-            // tokens that are not there: zeros, whatever the stage holds
-            if (!in || ka >= room) wa = 0u;
-            if (!in || ka + 1 >= room) wb = 0u;
-            if ((wa & 0x7fffu) > 0x7c00u) {
-              atomicMin(&pieces[u].nan_at, (t0 + t) * TILE_KEYS + ka);
-              wa = 0u;
-            }
-            if ((wb & 0x7fffu) > 0x7c00u) {
-              atomicMin(&pieces[u].nan_at, (t0 + t) * TILE_KEYS + ka + 1);
-              wb = 0u;
-            }
-            const uint32_t step = __byte_perm(wa, wb, 0x5410), zero = __byte_perm(wa, wb, 0x7632);
             uint32_t ra[2 * WPL], rb[2 * WPL];   // pairs of elements of either token
 #pragma unroll
             for (int w = 0; w < WPL; ++w) {
@@ -513,19 +511,12 @@ __device__ void unpack_role(const Kv4AttnParams& p, const Bars& br, uint32_t bas
             const int e = g * (D / 8);
             const uint32_t row = dst + (e >> 6) * BOX_BYTES + ka * 128;
 #pragma unroll
-            for (int cc = 0; cc < WPL / 2; ++cc) {
-              const int c2 = WPL == 4 ? (cc ^ (g & 1)) : cc;
-              const int chunk = ((e & 63) >> 3) + c2;
-              const uint32_t* pa = ra;
-              const uint32_t* pb = rb;
-              uint32_t a4[4], b4[4];
-#pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                a4[z] = (WPL == 4 && c2 == 1) ? pa[(4 + z) % (2 * WPL)] : pa[z];
-                b4[z] = (WPL == 4 && c2 == 1) ? pb[(4 + z) % (2 * WPL)] : pb[z];
-              }
-              sts128(row + ((chunk ^ (ka & 7)) * 16), a4[0], a4[1], a4[2], a4[3]);
-              sts128(row + 128 + ((chunk ^ ((ka + 1) & 7)) * 16), b4[0], b4[1], b4[2], b4[3]);
+            for (int c = 0; c < WPL / 2; ++c) {
+              const int chunk = ((e & 63) >> 3) + c;
+              sts128(row + ((chunk ^ (ka & 7)) * 16), ra[4 * c], ra[4 * c + 1], ra[4 * c + 2],
+                     ra[4 * c + 3]);
+              sts128(row + 128 + ((chunk ^ ((ka + 1) & 7)) * 16), rb[4 * c], rb[4 * c + 1],
+                     rb[4 * c + 2], rb[4 * c + 3]);
             }
           }
         }
@@ -538,99 +529,140 @@ __device__ void unpack_role(const Kv4AttnParams& p, const Bars& br, uint32_t bas
 }
 
 // ------------------------------------------------------------------ softmax
-// Scores of 32 columns before the factor rho: C in sr becomes ks C + kz sigma,
-// the steps and zeros from shared memory at `par`.
-__device__ __forceinline__ void scores32(uint32_t (&sr)[32], uint32_t par, uint64_t sigma2) {
+// A softmax warp holds its 32 rows as the fragments of four m16n8 products
+// (tmem_ld_16x256_x8): thread (g, t) has the rows g, g + 8, g + 16, g + 24 and of
+// every 8 columns 2t and 2t + 1.  So the steps and zeros of two tokens, which
+// every row needs, are one 16-byte read for four rows instead of one for
+// each (LDS was the kernel's busiest pipe with a row to a thread), and the row
+// sums are joined over the four lanes of a row once, at the end of a piece.
+//
+// Scores in log2 units are s = C ks' + kz' sigma with ks' = ks scale log2(e)
+// 2^(24 - Q_SHIFT) and kz' = kz scale log2(e), which the unpacking warps
+// prepare; q is scaled by 2^Q_SHIFT for every row, so the exponent s - m + 5 is
+// two fused multiply-adds.  A row whose magnitudes that scale would take out
+// of fp16's range has a scale of its own, and its C a factor `f`.
+struct Rows {
+  uint64_t sigma2[4];   // sum of q, twice
+  float f[4];
+  int sees[4];          // tokens that the row sees
+};
+
+// P = 2^(s - m + P_SHIFT) of 64 of the rows' columns as fp16 pairs in pk, added to acc.
+// SLOW: with the rows' factors; the columns behind a row's last token and the
+// blocks that are not in `on` are 0; and s is rounded before the sum, as the
+// reference was formed, which very large scores need.
+template <bool SLOW>
+__device__ __forceinline__ void weights64(uint32_t (&pk)[2][16], uint64_t (&acc)[4], uint32_t tS,
+                                          uint32_t par, const Rows& r, const uint64_t (&nm2)[4],
+                                          int key0, uint32_t on) {
+  const int t = threadIdx.x & 3;
+  uint32_t x[2][32];
+  tmem_ld_16x256_x8(tS, x[0]);
+  tmem_ld_16x256_x8(tS + (16u << 16), x[1]);
+  tmem_wait_ld();
 #pragma unroll
-  for (int j = 0; j < 32; j += 4) {
-    uint32_t ks[4], kz[4];
-    lds128(ks, par + 4 * j);
-    lds128(kz, par + TILE_KEYS * 4 + 4 * j);
+  for (int j = 0; j < 8; ++j) {
+    uint32_t k[4];
+    lds128(k, par + 64 * j + 16 * t);
+    const uint64_t ks = f2_pack(__uint_as_float(k[0]), __uint_as_float(k[1]));
+    const uint64_t kz = f2_pack(__uint_as_float(k[2]), __uint_as_float(k[3]));
 #pragma unroll
-    for (int e = 0; e < 4; e += 2) {
-      const uint64_t b =
-          f2_mul(f2_pack(__uint_as_float(kz[e]), __uint_as_float(kz[e + 1])), sigma2);
-      float a0, a1;
-      f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[j + e]), __uint_as_float(sr[j + e + 1])),
-                       f2_pack(__uint_as_float(ks[e]), __uint_as_float(ks[e + 1])), b),
-                a0, a1);
-      sr[j + e] = __float_as_uint(a0);
-      sr[j + e + 1] = __float_as_uint(a1);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t* c = x[i >> 1] + 4 * j + 2 * (i & 1);
+      uint64_t c2 = f2_pack(__uint_as_float(c[0]), __uint_as_float(c[1]));
+      float p0, p1;
+      if (SLOW) {
+        c2 = f2_mul(c2, f2_pack(r.f[i], r.f[i]));
+        f2_unpack(f2_add(f2_fma(c2, ks, f2_mul(kz, r.sigma2[i])), nm2[i]), p0, p1);
+        const int left = r.sees[i] - key0 - 2 * t;   // columns 8j, 8j + 1 below it
+        const bool in = (on >> (j >> 1)) & 1u;
+        if (8 * j >= left || !in) p0 = -INFINITY;
+        if (8 * j + 1 >= left || !in) p1 = -INFINITY;
+      } else {
+        f2_unpack(f2_fma(c2, ks, f2_fma(kz, r.sigma2[i], nm2[i])), p0, p1);
+      }
+      p0 = ex2_approx(p0);
+      p1 = ex2_approx(p1);
+      acc[i] = f2_add(acc[i], f2_pack(p0, p1));
+      pk[i >> 1][2 * j + (i & 1)] = pack_f16x2(p0, p1);
     }
   }
 }
 
-// P = 2^(u rho + nm) of one row as fp16 pairs in pk, its row sum, and the
-// largest exponent in `top` (NaN if one is).  MASKED: the columns behind `lim`
-// and the blocks that are not in `have` are 0; and the product is rounded
-// before the sum, as the reference was formed, which very large scores need.
-template <bool MASKED>
-__device__ __forceinline__ float weights(uint32_t (&pk)[64], uint32_t tS, uint32_t par,
-                                         uint64_t sigma2, float rho, float nm, int lim,
-                                         uint32_t have, float& top) {
-  const uint64_t rho2 = f2_pack(rho, rho), nm2 = f2_pack(nm, nm);
-  uint64_t acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-  float mx[2] = {-INFINITY, -INFINITY};
-  // two halves of 64 columns in one copy of the code: the tile's loop has to
-  // fit the instruction cache beside the unpacking and MMA loops
+// The two halves of a tile; the rows' sums in `sum`.  The reference has to move
+// if a sum passes P_LIMIT, which bounds its terms.
+template <bool SLOW>
+__device__ __forceinline__ void weights(uint32_t (&pk)[2][2][16], uint32_t tS, uint32_t par,
+                                        const Rows& r, const float (&m)[4], int key0,
+                                        uint32_t have, float (&sum)[4]) {
+  uint64_t acc[4], nm2[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    acc[i] = f2_pack(0.f, 0.f);
+    nm2[i] = f2_pack(P_SHIFT - m[i], P_SHIFT - m[i]);
+  }
+  if (SLOW) {
+    // one copy of the code, which is seldom run
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        pk[0][0][j] = pk[1][0][j];
+        pk[0][1][j] = pk[1][1][j];
+      }
+      weights64<true>(pk[1], acc, tS + 64 * half, par + 512 * half, r, nm2, key0 + 64 * half,
+                      have >> (4 * half));
+    }
+  } else {
+    weights64<false>(pk[0], acc, tS, par, r, nm2, key0, have);
+    weights64<false>(pk[1], acc, tS + 64, par + 512, r, nm2, key0 + 64, have >> 4);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    f2_unpack(acc[i], a, b);
+    sum[i] = a + b;
+  }
+}
+
+// The largest scores of the rows, -inf for a row that sees no token.
+__device__ __forceinline__ void row_max(float (&m)[4], uint32_t tS, uint32_t par, const Rows& r,
+                                        int key0, uint32_t have) {
+  const int t = threadIdx.x & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = -INFINITY;
 #pragma unroll 1
   for (int half = 0; half < 2; ++half) {
-    uint32_t sr[2][32];
-    tmem_ld32(tS + 64 * half, sr[0]);
-    if (half == 1) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) pk[j] = pk[32 + j];
-    }
-    const int left = lim - 64 * half;
+    uint32_t x[2][32];
+    tmem_ld_16x256_x8(tS + 64 * half, x[0]);
+    tmem_ld_16x256_x8(tS + (16u << 16) + 64 * half, x[1]);
+    tmem_wait_ld();
     const uint32_t on = have >> (4 * half);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      tmem_wait_ld();
-      if (c < 1) tmem_ld32(tS + 64 * half + 32, sr[1]);
-      uint32_t(&x)[32] = sr[c];
-      scores32(x, par + 256 * half + 128 * c, sigma2);
+    for (int j = 0; j < 8; ++j) {
+      uint32_t k[4];
+      lds128(k, par + 512 * half + 64 * j + 16 * t);
+      const uint64_t ks = f2_pack(__uint_as_float(k[0]), __uint_as_float(k[1]));
+      const uint64_t kz = f2_pack(__uint_as_float(k[2]), __uint_as_float(k[3]));
+      const bool in = (on >> (j >> 1)) & 1u;
 #pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        const int col = 32 * c + j;
-        const uint64_t s2 = f2_pack(__uint_as_float(x[j]), __uint_as_float(x[j + 1]));
-        float p0, p1;
-        f2_unpack(MASKED ? f2_add(f2_mul(s2, rho2), nm2) : f2_fma(s2, rho2, nm2), p0, p1);
-        if (MASKED) {
-          const bool in = (on >> (col >> 4)) & 1u;
-          if (col > left || !in) p0 = -INFINITY;
-          if (col + 1 > left || !in) p1 = -INFINITY;
-        }
-        mx[(j >> 1) & 1] = fmax3(mx[(j >> 1) & 1], p0, p1);
-        p0 = ex2_approx(p0);
-        p1 = ex2_approx(p1);
-        acc[(j >> 1) & 1] = f2_add(acc[(j >> 1) & 1], f2_pack(p0, p1));
-        pk[32 + 16 * c + (j >> 1)] = pack_f16x2(p0, p1);
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t* c = x[i >> 1] + 4 * j + 2 * (i & 1);
+        const uint64_t c2 = f2_mul(f2_pack(__uint_as_float(c[0]), __uint_as_float(c[1])),
+                                   f2_pack(r.f[i], r.f[i]));
+        float s0, s1;
+        f2_unpack(f2_fma(c2, ks, f2_mul(kz, r.sigma2[i])), s0, s1);
+        const int left = r.sees[i] - key0 - 64 * half - 2 * t;
+        if (in && 8 * j < left) m[i] = fmaxf(m[i], s0);
+        if (in && 8 * j + 1 < left) m[i] = fmaxf(m[i], s1);
       }
     }
   }
-  float a, b;
-  f2_unpack(f2_add(acc[0], acc[1]), a, b);
-  top = fmaxf(mx[0], mx[1]);
-  return a + b;
-}
-
-// The largest score of a row before the factor rho, -inf if it sees none.
-__device__ __forceinline__ float row_max(uint32_t tS, uint32_t par, uint64_t sigma2, int lim,
-                                         uint32_t have) {
-  float m = -INFINITY;
-#pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    uint32_t x[32];
-    tmem_ld32(tS + 32 * c, x);
-    tmem_wait_ld();
-    scores32(x, par + 128 * c, sigma2);
-    const int n = lim - 32 * c;
-    const uint32_t on = have >> (2 * c);
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j <= n && ((on >> (j >> 4)) & 1u)) m = fmaxf(m, __uint_as_float(x[j]));
+  for (int i = 0; i < 4; ++i) {
+    m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], 1));
+    m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], 2));
   }
-  return m;
 }
 
 // Barrier of the 256 softmax threads, bounded as every wait; false if the
@@ -750,9 +782,8 @@ __device__ void softmax_role(const Kv4AttnParams& p, const Bars& br, uint32_t ba
     q.n = pieces[u].n;
     q.len = pieces[u].len;
     const int rows = pieces[u].rows, row = pieces[u].row0 + w * TILE_ROWS + t;
-    const int sees = kv4_limit(p, q, row, rows);       // tokens that the row sees
-    float rho = 0.f;
-    uint64_t sigma2 = 0;
+    Rows r;
+    bool odd;               // some row of the warp has a factor
     // ---- q of this row: fp16 in shared memory, in the order of the codes
     {
       uint4 qw[D / 8];
@@ -768,11 +799,23 @@ __device__ void softmax_role(const Kv4AttnParams& p, const Bars& br, uint32_t ba
           sum += f.x + f.y;
         }
       }
-      float up, down;
-      kv4_row_scale(am, up, down);
-      rho = p.scale_log2 * down * 16777216.f;
-      const float sg = sum * up * 5.9604644775390625e-8f;
-      sigma2 = f2_pack(sg, sg);
+      float up = Q_SCALE, f = 1.f;
+      if (!(am == 0.f || (am < 255.f && am >= 6.1035156e-5f))) {
+        float down;
+        kv4_row_scale(am, up, down);
+        f = down * Q_SCALE;
+      }
+      odd = __any_sync(0xffffffffu, f != 1.f);
+      const int sees = kv4_limit(p, q, row, rows);
+      // to the threads that hold the row's fragments
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int from = 8 * i + ((threadIdx.x & 31) >> 2);
+        const float sg = __shfl_sync(0xffffffffu, sum, from);
+        r.sigma2[i] = f2_pack(sg, sg);
+        r.f[i] = __shfl_sync(0xffffffffu, f, from);
+        r.sees[i] = __shfl_sync(0xffffffffu, sees, from);
+      }
       if (q_uses > 0) {
         ok = wait_bar(br.q_empty, (q_uses - 1) & 1u, cx, SITE_Q_EMPTY);
         if (!__all_sync(0xffffffffu, ok)) return;
@@ -793,7 +836,14 @@ __device__ void softmax_role(const Kv4AttnParams& p, const Bars& br, uint32_t ba
       mbar_arrive(br.q_full);
     }
 
-    float m = -INFINITY, l = 0.f;
+    const int sees_min = __reduce_min_sync(
+        0xffffffffu, min(min(r.sees[0], r.sees[1]), min(r.sees[2], r.sees[3])));
+    float m[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+    }
     bool far = false;       // some row's reference is so large that roundings count
     for (int idx = 0; idx < n_kv; ++idx, ++tile) {
       if (!mine) continue;
@@ -805,52 +855,64 @@ __device__ void softmax_role(const Kv4AttnParams& p, const Bars& br, uint32_t ba
       s_phase ^= 1u;
       tc_fence_after();
       const uint32_t have = held[NRAW + slot];
-      const int lim = min(sees - (t0 + idx) * TILE_KEYS, TILE_KEYS) - 1;
-      const bool masked = __any_sync(0xffffffffu, lim < TILE_KEYS - 1) || have != 0xffu;
+      const int key0 = (t0 + idx) * TILE_KEYS;
+      const bool masked = sees_min < key0 + TILE_KEYS || have != 0xffu;
       const uint32_t par = base + C::OFF_PAR + slot * TILE_KEYS * 8;
 
       // P with the reference in hand; where that would pass fp16's range (or is
       // none yet), the reference first moves to the row's maximum
-      uint32_t pk[64];
-      float rsum = 0.f;
-      bool slow = masked || far;
+      uint32_t pk[2][2][16];
+      float sum[4];
 #pragma unroll 1
       for (int round = 0; round < 2; ++round) {
-        float top;
-        rsum = slow ? weights<true>(pk, tS, par, sigma2, rho, P_SHIFT - m, lim, have, top)
-                    : weights<false>(pk, tS, par, sigma2, rho, P_SHIFT - m, lim, have, top);
-        if (round == 1 || !__any_sync(0xffffffffu, top > P_LIMIT_LOG2)) break;
-        const float rmax = row_max(tS, par, sigma2, lim, have);
-        const float m_new = rmax == -INFINITY ? m : fmaxf(m, __fmul_rn(rmax, rho));
-        const float alpha = m_new == m ? 1.f : ex2_approx(m - m_new);
+        if (masked || far || odd)
+          weights<true>(pk, tS, par, r, m, key0, have, sum);
+        else
+          weights<false>(pk, tS, par, r, m, key0, have, sum);
+        const float top = fmaxf(fmaxf(sum[0], sum[1]), fmaxf(sum[2], sum[3]));
+        if (round == 1 || !__any_sync(0xffffffffu, top > P_LIMIT)) break;
+        float rmax[4], alpha[4];
+        row_max(rmax, tS, par, r, key0, have);
+        bool big = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float m_new = fmaxf(m[i], rmax[i]);
+          alpha[i] = m_new == m[i] ? 1.f : ex2_approx(m[i] - m_new);
+          l[i] *= alpha[i];
+          m[i] = m_new;
+          big |= fabsf(m_new) > 4096.f && m_new != -INFINITY;
+        }
+        far = __any_sync(0xffffffffu, big);
         if (idx > 0) {
           // O already holds every earlier P V of this tile: the commit that
           // signalled S for this step fires only after them
 #pragma unroll 1
-          for (int cc = 0; cc < D / 32; ++cc) {
-            uint32_t o[32];
-            tmem_ld32(tO + cc * 32, o);
-            tmem_wait_ld();
+          for (int cc = 0; cc < D / 64; ++cc) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-            tmem_st32(tO + cc * 32, o);
+            for (int hh = 0; hh < 2; ++hh) {
+              uint32_t o[32];
+              const uint32_t at = tO + (static_cast<uint32_t>(16 * hh) << 16) + cc * 64;
+              tmem_ld_16x256_x8(at, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha[2 * hh + ((j >> 1) & 1)]);
+              tmem_st_16x256_x8(at, o);
+            }
           }
           tmem_wait_st();
         }
-        l *= alpha;
-        m = m_new;
-        far = __any_sync(0xffffffffu, fabsf(m) > 4096.f && m != -INFINITY);
-        slow = masked || far;
       }
-      l += rsum;
-      tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(br.p_half(w));
-      tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(br.p_full(w));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) l[i] += sum[i];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        tmem_st_16x128_x8(tS + 32 * half, pk[half][0]);
+        tmem_st_16x128_x8(tS + (16u << 16) + 32 * half, pk[half][1]);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(half == 0 ? br.p_half(w) : br.p_full(w));
+      }
     }
 
     // ---- the piece's rows: finished, or a partial in the workspace
@@ -858,33 +920,64 @@ __device__ void softmax_role(const Kv4AttnParams& p, const Bars& br, uint32_t ba
       ok = wait_bar(br.o_done(w), units_w & 1u, cx, SITE_O_DONE);
       if (!__all_sync(0xffffffffu, ok)) return;
       tc_fence_after();
-      const bool bad = *reinterpret_cast<volatile int*>(&pieces[u].nan_at) < sees;
-      const bool whole = pieces[u].whole, row_ok = row < pieces[u].rows;
-      const int h = pieces[u].h, lrow = w * TILE_ROWS + t;
-      q.first = pieces[u].first;
-      float* slot = p.partials + (2ll * blockIdx.x + (static_cast<int>(blockIdx.x) == pieces[u].c0)) *
+      const int lane = threadIdx.x & 31, g = lane >> 2, tt = lane & 3;
+      const int nan_at = *reinterpret_cast<volatile int*>(&pieces[u].nan_at);
+      const bool whole = pieces[u].whole;
+      const int n_rows = pieces[u].rows, h = pieces[u].h, row0 = pieces[u].row0;
+      float* part = p.partials + (2ll * blockIdx.x + (static_cast<int>(blockIdx.x) == pieces[u].c0)) *
                                      KV4C_PIECE_FLOATS;
-#pragma unroll 1
-      for (int cc = 0; cc < D / 32; ++cc) {
-        uint32_t o[32];
-        tmem_ld32(tO + cc * 32, o);
-        tmem_wait_ld();
-        if (row_ok) {
+      long long at[4];                 // of the row's first element in out
+      float inv[4];
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            float4 a = make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]),
-                                   __uint_as_float(o[j + 2]), __uint_as_float(o[j + 3]));
-            if (bad) a.x = a.y = a.z = a.w = __uint_as_float(0x7fffffffu);
-            if (whole)
-              kv4_store(p, q.first, h, row, cc * 32 + j, D, a, m - P_SHIFT, l);
-            else
-              *reinterpret_cast<float4*>(slot + lrow * D + cc * 32 + j) = a;
+      for (int i = 0; i < 4; ++i) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+        const int lrow = w * TILE_ROWS + quarter * 32 + 8 * i + g;
+        const int tok = (row0 + lrow) / p.group;
+        at[i] = row0 + lrow >= n_rows ? -1
+                : whole ? (static_cast<long long>(pieces[u].first) + tok) * p.Hq + h * p.group +
+                              (row0 + lrow - tok * p.group)
+                        : lrow;
+        // a row that saw no token has l = 0 and O = 0
+        inv[i] = !whole ? 1.f : l[i] == 0.f ? 0.f : 1.f / l[i];
+        if (nan_at < r.sees[i]) inv[i] = __uint_as_float(0x7fffffffu);
+        if (at[i] >= 0 && tt == 0) {
+          if (whole) {
+            p.lse[at[i]] = l[i] == 0.f ? -INFINITY
+                                       : (m[i] - P_SHIFT + log2f(l[i])) * 0.69314718055994530942f;
+          } else {
+            part[UNIT_ROWS * D + lrow] = m[i];
+            part[UNIT_ROWS * D + UNIT_ROWS + lrow] = l[i];
           }
         }
       }
-      if (row_ok && !whole) {
-        slot[UNIT_ROWS * D + lrow] = m;
-        slot[UNIT_ROWS * D + UNIT_ROWS + lrow] = l;
+#pragma unroll 1
+      for (int cc = 0; cc < D / 64; ++cc) {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t o[32];
+          tmem_ld_16x256_x8(tO + (static_cast<uint32_t>(16 * hh) << 16) + cc * 64, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const int i = 2 * hh + b;
+            if (at[i] < 0) continue;
+            const long long e = at[i] * D + cc * 64 + 2 * tt;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float y0 = __uint_as_float(o[4 * j + 2 * b]) * inv[i];
+              const float y1 = __uint_as_float(o[4 * j + 2 * b + 1]) * inv[i];
+              if (!whole)
+                *reinterpret_cast<float2*>(part + e + 8 * j) = make_float2(y0, y1);
+              else if (p.out_f32)
+                *reinterpret_cast<float2*>(static_cast<float*>(p.out) + e + 8 * j) =
+                    make_float2(y0, y1);
+              else
+                *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + e + 8 * j) =
+                    p.q_f16 ? pack_f16x2(y0, y1) : pack_bf16x2(y0, y1);
+            }
+          }
+        }
       }
       tc_fence_before();
       mbar_arrive(br.o_free(w));
