@@ -9,18 +9,28 @@
 // The codes go to the matrix instructions as they are, and the steps and
 // zeros are applied in fp32 around them, so nothing of K or V is rounded:
 //     q . k   = ks (q . codeK) + kz sum(q)
-//     sum p v = sum (p vs) codeV + sum p vz
+//     sum p v = sum (p vs) (codeV - 8) + sum p (vz + 8 vs)
 // * A nibble under the mask 0x000f is a subnormal fp16 number, code 2^-24,
 //   and under 0x00f0 it is code 2^-20: two codes become an operand register
 //   with one AND (and one shift for every second pair), no conversion.  The
 //   factor 16 between them is taken back in q (K: both lie in the sum over d,
 //   q there is divided by 16) and in the result (V: they are different rows
 //   of it).
+// * The 8 is taken off V's codes after the product, so that nothing is done to
+//   a single code: one more matrix instruction per block forms the sum of
+//   the rounded p vs.  Two blocks go through together, and the second enters
+//   as (15 - code) (-p vs), its complement, which costs nothing: what the two
+//   add to the accumulators is centred, so neither they nor their rounding,
+//   which is towards zero, grow with sum p vs.  (One request of 1M tokens, bf16,
+//   relative to the exact result: 0.0026 off with the codes as they are,
+//   0.0016 so, which is the rounding of the output.  Taking 8 off each code
+//   instead costs an operation a pair: 234 us against 200 us for 8 x 32K tokens
+//   of 32 heads.)
 // * q is scaled by a power of two per row so that its largest value lies in
 //   [2^14, 2^15): exact in fp16 for bf16 and fp16 inputs down to 2^-24 of the
 //   row's maximum.
-// * p vs = 2^(s - m + 8) vs is rounded to fp16 (2^-12 relative, finer than the
-//   output type) for the product with the codes; the row sum and the sum of
+// * p vs = 2^(s - m + 8) vs is rounded to fp16 (half a step, 2^-11 relative: no
+//   coarser than the output) for the product with the codes; the row sum and the sum of
 //   p vz use the fp32 values.  m is any reference that keeps p vs below
 //   2^15: it is moved, and the accumulators rescaled, only when a value of the
 //   block in hand would pass that, which one vote per block finds out.  The
@@ -131,6 +141,14 @@ __device__ __forceinline__ void code_pairs(uint32_t x, uint32_t (&p)[4]) {
   p[1] = x & 0x00f000f0u;
   p[2] = y & 0x000f000fu;
   p[3] = y & 0x00f000f0u;
+}
+// All four as codes (or 15 less the codes) times 2^-20.
+__device__ __forceinline__ void code_pairs_v(uint32_t x, uint32_t (&p)[4], bool complement) {
+  if (complement) x = ~x;   // part of the ANDs
+  p[0] = (x << 4) & 0x00f000f0u;
+  p[1] = x & 0x00f000f0u;
+  p[2] = (x >> 4) & 0x00f000f0u;
+  p[3] = (x >> 8) & 0x00f000f0u;
 }
 
 // A unit of which this CTA holds pieces: where its rows are, and the warps w0
@@ -385,7 +403,7 @@ __global__ void __launch_bounds__(THREADS, (Smem<D, NT>::CTAS))
     for (int j = 0; j < NT; ++j) lim_min = min(lim_min, min(lim[j][0], lim[j][1]));
     lim_min = __reduce_min_sync(0xffffffffu, lim_min);
 
-    float o[NT][2 * WPL][4];
+    float o[NT][2 * WPL][4], c8[NT][4];    // c8: what makes it codes less 8
     float mo[NT][2], l[NT][2], z[NT][2];   // mo = P_SHIFT - m
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -393,6 +411,7 @@ __global__ void __launch_bounds__(THREADS, (Smem<D, NT>::CTAS))
       for (int i = 0; i < 2 * WPL; ++i)
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[j][i][c] = 0.f;
+      c8[j][0] = c8[j][1] = c8[j][2] = c8[j][3] = 0.f;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         mo[j][c] = INFINITY;
@@ -492,6 +511,7 @@ __global__ void __launch_bounds__(THREADS, (Smem<D, NT>::CTAS))
             mo[j][cc] = mo_new;
             l[j][cc] *= alpha;
             z[j][cc] *= alpha;
+            c8[j][cc] *= alpha;
 #pragma unroll
             for (int i2 = 0; i2 < 2 * WPL; ++i2) {
               o[j][i2][cc] *= alpha;
@@ -504,7 +524,8 @@ __global__ void __launch_bounds__(THREADS, (Smem<D, NT>::CTAS))
         for (int x = 0; x < 2; ++x) {
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) {
-            const float vz = kv4_params(vp[x][q4 >> 1]).y;
+            const float2 vs = kv4_params(vp[x][q4 >> 1]);
+            const float vz = fmaf(8.f, vs.x, vs.y);   // the value of code 8
             const int cc = q4 & 1;
             l[j][cc] += e[x][q4];
             // a hidden token's zero may be NaN: 0 times it is not 0
@@ -523,13 +544,26 @@ __global__ void __launch_bounds__(THREADS, (Smem<D, NT>::CTAS))
       }
       __syncwarp();
       issue_next();   // everything of the stage is in registers
+      // block 0 adds p vs code, and p vs times -8; block 1 adds -p vs (15 - code),
+      // and -p vs times -7
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          if (x == 1) {
+            pb[j][x][0] ^= 0x80008000u;
+            pb[j][x][1] ^= 0x80008000u;
+          }
+          const uint32_t k = x == 0 ? 0x80808080u : 0x80708070u;   // -8 2^-20, -7 2^-20
+          mma_f16(c8[j], k, k, k, k, pb[j][x][0], pb[j][x][1]);
+        }
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int w = 0; w < WPL; ++w) {
           uint32_t a[4], b[4];
-          code_pairs(v0[x][w], a);
-          code_pairs(v1[x][w], b);
+          code_pairs_v(v0[x][w], a, x == 1);
+          code_pairs_v(v1[x][w], b, x == 1);
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             mma_f16(o[j][2 * w], a[0], a[1], b[0], b[1], pb[j][x][0], pb[j][x][1]);
@@ -566,6 +600,15 @@ __global__ void __launch_bounds__(THREADS, (Smem<D, NT>::CTAS))
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
+      for (int i2 = 0; i2 < 2 * WPL; ++i2)
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          o[j][i2][cc] += c8[j][cc];
+          o[j][i2][2 + cc] += c8[j][cc];
+        }
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
       for (int cc = 0; cc < 2; ++cc)
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {
@@ -573,9 +616,9 @@ __global__ void __launch_bounds__(THREADS, (Smem<D, NT>::CTAS))
           z[j][cc] += __shfl_xor_sync(0xffffffffu, z[j][cc], x);
         }
     auto values = [&](int j, int cc, int w) {   // elements g d/8 + 4 w .. + 3 of column 2 t + cc
-      return make_float4(fmaf(o[j][2 * w][cc], 16777216.f, z[j][cc]),
+      return make_float4(fmaf(o[j][2 * w][cc], 1048576.f, z[j][cc]),
                          fmaf(o[j][2 * w][2 + cc], 1048576.f, z[j][cc]),
-                         fmaf(o[j][2 * w + 1][cc], 16777216.f, z[j][cc]),
+                         fmaf(o[j][2 * w + 1][cc], 1048576.f, z[j][cc]),
                          fmaf(o[j][2 * w + 1][2 + cc], 1048576.f, z[j][cc]));
     };
     const bool head = first < me * per;              // its blocks begin before this warp's
