@@ -437,11 +437,12 @@ ra_status ring_attn_kv4_read(const void* cache, const int32_t* slots, void* k, v
 
 /*
  * ring_attn_kv4_workspace_size -- bytes of device workspace that any call of
- * ring_attn_kv4_fwd needs.  The workspace is zeroed once, before its first
- * call; each call leaves it ready for the next one.  Calls that may run at the same
- * time (streams, replays of captured graphs) need one each.  After an
- * error from ring_attn_check_status it has to be zeroed again.
+ * ring_attn_kv4_fwd needs.  Its first RA_KV4_COUNTER_BYTES are zeroed once,
+ * before its first call; each call leaves them zero.  Calls that may run at
+ * the same time (streams, replays of captured graphs) need a workspace each.
+ * After an error from ring_attn_check_status they have to be zeroed again.
  */
+enum { RA_KV4_COUNTER_BYTES = 16384 };
 ra_status ring_attn_kv4_workspace_size(size_t* bytes);
 
 /*

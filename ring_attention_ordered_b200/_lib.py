@@ -159,6 +159,7 @@ def ring_attn_merge(o_a, lse_a, o_b, lse_b, o_out, lse_out, rows, d, stream=0):
 
 
 RA_BF16, RA_FP16, RA_FP32 = 0, 1, 2
+KV4_COUNTER_BYTES = 16384   # of a kv4 workspace, zero before its first call
 
 
 def ring_attn_kv4_plan(lens, add, table, pool, lens_out, table_out, pool_out, cu, slots, shortage,

@@ -528,12 +528,14 @@ def _read(cache, slots, dtype, k, v, index, P, Hkv, page, d, sh):
 
 
 def kv4_workspace(device="cuda") -> torch.Tensor:
-    """A workspace for ``kv4_fwd``, zeroed as it has to be.  One serves any
-    number of calls that run one after the other."""
+    """A workspace for ``kv4_fwd``, its counters zeroed as they have to be.
+    One serves any number of calls that run one after the other."""
     global _workspace_bytes
     if _workspace_bytes is None:
         _workspace_bytes = _lib.ring_attn_kv4_workspace_size()
-    return torch.zeros(_workspace_bytes, dtype=torch.uint8, device=device)
+    w = torch.empty(_workspace_bytes, dtype=torch.uint8, device=device)
+    w[:_lib.KV4_COUNTER_BYTES].zero_()
+    return w
 
 
 def kv4_fwd(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
@@ -549,7 +551,7 @@ def kv4_fwd(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens: tor
     tokens are the last of these.  Returns (out [T, Hq, d] of q's type or
     ``out_dtype`` float32, lse fp32 [T, Hq]); rows from cu[R] on are not
     written.  ``max_q`` bounds the query tokens of a request (default T).
-    ``workspace`` (``kv4_workspace``) is allocated and zeroed if omitted."""
+    ``workspace`` (``kv4_workspace``) is made for the call if omitted."""
     T, Hq, dq, qs = _check_rows(q, "q")
     P, Hkv, page, d = _cache_shape(cache)
     if dq != d or Hq % Hkv != 0 or Hq < 1:

@@ -221,6 +221,7 @@ constexpr size_t KV4_COUNTER_BYTES = 3 * KV4_MAX_CTAS * 4;
 constexpr size_t KV4C_COUNTER_BYTES = 3 * KV4C_MAX_CTAS * 4;
 constexpr size_t KV4_PARTIAL_BYTES = 2ull * KV4C_MAX_CTAS * KV4C_PIECE_FLOATS * 4;
 static_assert(KV4_PARTIAL_BYTES >= 2ull * KV4_MAX_CTAS * KV4_PIECE_FLOATS * 4, "partials");
+static_assert(KV4_COUNTER_BYTES + KV4C_COUNTER_BYTES <= 16384, "RA_KV4_COUNTER_BYTES");
 static_assert((KV4_COUNTER_BYTES + KV4C_COUNTER_BYTES) % 16 == 0, "partials are 16-byte aligned");
 constexpr size_t KV4_WORKSPACE_BYTES = KV4_COUNTER_BYTES + KV4C_COUNTER_BYTES + KV4_PARTIAL_BYTES;
 

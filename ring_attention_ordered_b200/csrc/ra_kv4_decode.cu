@@ -114,6 +114,15 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same onto zeros.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -426,10 +435,6 @@ __global__ void __launch_bounds__(THREADS, (Smem<D, NT>::CTAS))
       const uint32_t held = (have >> (2 * s)) & 3u;
       const uint32_t blk = ring + s * (2 * L::BLOCK_BYTES);
       float c[NT][2][4];
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) c[j][x][0] = c[j][x][1] = c[j][x][2] = c[j][x][3] = 0.f;
       uint32_t kp[2][2], vp[2][2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -448,7 +453,10 @@ __global__ void __launch_bounds__(THREADS, (Smem<D, NT>::CTAS))
           code_pairs(k1[w], b);
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            mma_f16(c[j][x], a[0], b[0], a[1], b[1], qf[j][2 * w][0], qf[j][2 * w][1]);
+            if (w == 0)
+              mma_f16_first(c[j][x], a[0], b[0], a[1], b[1], qf[j][0][0], qf[j][0][1]);
+            else
+              mma_f16(c[j][x], a[0], b[0], a[1], b[1], qf[j][2 * w][0], qf[j][2 * w][1]);
             mma_f16(c[j][x], a[2], b[2], a[3], b[3], qf[j][2 * w + 1][0], qf[j][2 * w + 1][1]);
           }
         }

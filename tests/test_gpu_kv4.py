@@ -103,6 +103,23 @@ def test_plan_that_cannot_be_met_changes_nothing(ra, in_place):
     assert check_plan(ra, lens, [0] * 9, table, pool, 16, 0, in_place) == 0
 
 
+def test_plan_partly_in_place(ra):
+    """Each of the three states by itself in the input's place."""
+    r = random.Random(12)
+    lens, add, table, pool = random_plan(r, 70, 6, 16, 300, 30)
+    want = kv4.kv4_plan(lens, add, table, pool, 16, 2500)
+    for place in (0, 1, 2):
+        args = [i32(lens), i32(add), i32(table), i32(pool)]
+        out = [torch.empty_like(args[0]), torch.empty_like(args[2]), torch.empty_like(args[3]),
+               i32([0] * 71), i32([0] * 2500), i32([0])]
+        out[place] = args[(0, 2, 3)[place]]
+        got = ra.kv4_plan(*args, 16, 2500, out=out)
+        for g, w in zip(got, want):
+            assert np.array_equal(g.cpu().numpy().reshape(-1), np.asarray(w).reshape(-1))
+    with pytest.raises(Exception):
+        ra.kv4_plan(*args, 16, 2500, out=[args[1]] + out[1:])   # overlaps `add`
+
+
 def test_plan_of_no_request(ra):
     got = ra.kv4_plan(i32([]), i32([]), torch.empty((0, 3), dtype=torch.int32, device="cuda"),
                       ra.kv4_pool(5), 16, 4)
@@ -323,8 +340,8 @@ class Batch:
                 tol = tol + (w[:, h] * (ds + 2.0 ** -18)) @ av
                 tol = tol * (1 + 2 * half) + half * np.abs(ref[:, h]) + 1e-30
                 err = np.abs(got - ref[:, h])
-                assert (err <= tol).all(), (i, h, float((err / tol).max()))
-                worst = max(worst, float((err / tol).max()))
+                assert (err <= tol).all(), (i, h, float((err / tol).max(initial=0.0)))
+                worst = max(worst, float((err / tol).max(initial=0.0)))
                 rl, gl = ref_lse[:, h], lse[at:at + m, h]
                 none = np.isneginf(rl)
                 assert np.array_equal(none, np.isneginf(gl)) and (got[none] == 0).all()
@@ -523,6 +540,62 @@ def test_pages_out_of_range_are_left_out_and_reported(ra):
     ra.kv4_fwd(b.q.cuda(), b.cache, b.table.clamp(min=0), lens, cu=cu)
     with pytest.raises(_lib.RingAttnError):
         ra.check_status()
+
+
+def test_many_requests(ra):
+    """More requests than threads, most of them short or empty."""
+    r = random.Random(5)
+    lens = [r.choice([0, 1, 5, 17, 40]) for _ in range(700)]
+    attend(ra, Batch(ra, lens, [1] * 700, 2, 1, 64, 16, torch.bfloat16, 41))
+    n = [r.choice([1, 1, 2, 0, 40]) for _ in range(600)]
+    attend(ra, Batch(ra, [max(a, b) for a, b in zip(lens, n)], n, 4, 1, 64, 16, torch.float16, 42))
+
+
+def test_long_sums_keep_their_precision(ra):
+    """Weights spread over many tokens: the result is small beside the values,
+    and nothing that grows with the number of tokens may show.  Against the
+    cached values in 64 bits, as a norm: the output's rounding (rms 2^-11 / sqrt 12
+    to twice that) and as much again for rounding p."""
+    L, d = 60000, 64
+    g = torch.Generator().manual_seed(3)
+    k = (0.3 * torch.randn(L, 1, d, generator=g)).to(torch.float16)
+    v = torch.randn(L, 1, d, generator=g).to(torch.float16)
+    q = torch.randn(1, 8, d, generator=g).to(torch.float16)
+    cache = ra.kv4_cache(-(-L // 64), 1, d, 64)
+    ra.kv4_append(k.cuda(), v.cuda(), i32(list(range(L))), cache)
+    table = i32([list(range(cache.shape[0]))])
+    kc, vc = (kv4.kv4_values(*oracle_values(x)) for x in (k, v))
+    ref, _, _ = kv4.kv4_attention(q.double().numpy(), kc, vc, 1, True, 0.125)
+    out, _ = ra.kv4_fwd(q.cuda(), cache, table, i32([L]))
+    err = np.linalg.norm(out.double().cpu().numpy() - ref) / np.linalg.norm(ref)
+    assert err < 2 * 2.0 ** -10 / math.sqrt(12), err
+
+
+def test_two_graphs_share_a_workspace_one_after_the_other(ra):
+    """Two captured calls with one workspace, replayed in turn, and a third
+    with its own on another stream at the same time."""
+    b = [Batch(ra, lens, [n] * len(lens), 4, 2, 64, 16, torch.bfloat16, 50 + i)
+         for i, (lens, n) in enumerate((([3000, 40, 777], 1), ([900, 2000], 60), ([5000], 1)))]
+    want = [attend(ra, x) for x in b]
+    shared, own = ra.kv4_workspace(), ra.kv4_workspace()
+    side = torch.cuda.Stream()
+    graphs, outs, qs = [], [], [x.q.cuda() for x in b]
+    torch.cuda.synchronize()
+    for i, x in enumerate(b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(ra.kv4_fwd(qs[i], x.cache, x.table, x.len_t, cu=x.cu, max_q=max(x.n),
+                                   workspace=own if i == 2 else shared))
+        graphs.append(g)
+    for _ in range(5):
+        with torch.cuda.stream(side):
+            graphs[2].replay()
+        graphs[0].replay()
+        graphs[1].replay()
+    torch.cuda.synchronize()
+    ra.check_status()
+    for o, w in zip(outs, want):
+        assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
 
 
 def test_on_another_stream(ra):
