@@ -152,12 +152,14 @@ __device__ __forceinline__ void code_pairs(uint32_t x, uint32_t (&p)[4]) {
   p[3] = y & 0x00f000f0u;
 }
 // All four as codes (or 15 less the codes) times 2^-20.
-__device__ __forceinline__ void code_pairs_v(uint32_t x, uint32_t (&p)[4], bool complement) {
-  if (complement) x = ~x;   // part of the ANDs
-  p[0] = (x << 4) & 0x00f000f0u;
-  p[1] = x & 0x00f000f0u;
-  p[2] = (x >> 4) & 0x00f000f0u;
-  p[3] = (x >> 8) & 0x00f000f0u;
+template <bool COMPLEMENT>
+__device__ __forceinline__ void code_pairs_v(uint32_t x, uint32_t (&p)[4]) {
+  const uint32_t m = 0x00f000f0u;
+  const uint32_t a = x << 4, b = x >> 4, c = x >> 8;
+  p[0] = COMPLEMENT ? ~a & m : a & m;
+  p[1] = COMPLEMENT ? ~x & m : x & m;
+  p[2] = COMPLEMENT ? ~b & m : b & m;
+  p[3] = COMPLEMENT ? ~c & m : c & m;
 }
 
 // A unit of which this CTA holds pieces: where its rows are, and the warps w0
@@ -338,16 +340,25 @@ __global__ void __launch_bounds__(THREADS, (Smem<D, NT>::CTAS))
       const int e0 = __shfl_sync(0xffffffffu, ent, 2 * (issued & 15));
       const int e1 = __shfl_sync(0xffffffffu, ent, 2 * (issued & 15) + 1);
       const uint32_t s = (it0 + issued) % STAGES;
-      have = (have & ~(3u << (2 * s))) | ((e0 >= 0 ? 1u : 0u) << (2 * s)) |
-             ((e1 >= 0 ? 2u : 0u) << (2 * s));
-      if (lane == 0) {
-        const uint32_t bar = bars + 8 * s, dst = ring + s * (2 * L::BLOCK_BYTES);
-        mbar_arrive_expect_tx(bar, L::BLOCK_BYTES * ((e0 >= 0) + (e1 >= 0)));
-        if (e0 >= 0)
-          bulk_load(dst, p.cache + static_cast<long long>(e0) * L::BLOCK_BYTES, L::BLOCK_BYTES, bar);
-        if (e1 >= 0)
-          bulk_load(dst + L::BLOCK_BYTES, p.cache + static_cast<long long>(e1) * L::BLOCK_BYTES,
-                    L::BLOCK_BYTES, bar);
+      const uint32_t bar = bars + 8 * s, dst = ring + s * (2 * L::BLOCK_BYTES);
+      const uint8_t* src = p.cache + static_cast<long long>(e0) * L::BLOCK_BYTES;
+      if (e0 >= 0 && e1 == e0 + 1) {
+        // side by side in one page: one copy
+        have |= 3u << (2 * s);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(bar, 2 * L::BLOCK_BYTES);
+          bulk_load(dst, src, 2 * L::BLOCK_BYTES, bar);
+        }
+      } else {
+        have = (have & ~(3u << (2 * s))) | ((e0 >= 0 ? 1u : 0u) << (2 * s)) |
+               ((e1 >= 0 ? 2u : 0u) << (2 * s));
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, L::BLOCK_BYTES * ((e0 >= 0) + (e1 >= 0)));
+          if (e0 >= 0) bulk_load(dst, src, L::BLOCK_BYTES, bar);
+          if (e1 >= 0)
+            bulk_load(dst + L::BLOCK_BYTES,
+                      p.cache + static_cast<long long>(e1) * L::BLOCK_BYTES, L::BLOCK_BYTES, bar);
+        }
       }
       ++issued;
     };
@@ -570,8 +581,13 @@ __global__ void __launch_bounds__(THREADS, (Smem<D, NT>::CTAS))
 #pragma unroll
         for (int w = 0; w < WPL; ++w) {
           uint32_t a[4], b[4];
-          code_pairs_v(v0[x][w], a, x == 1);
-          code_pairs_v(v1[x][w], b, x == 1);
+          if (x == 0) {
+            code_pairs_v<false>(v0[x][w], a);
+            code_pairs_v<false>(v1[x][w], b);
+          } else {
+            code_pairs_v<true>(v0[x][w], a);
+            code_pairs_v<true>(v1[x][w], b);
+          }
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             mma_f16(o[j][2 * w], a[0], a[1], b[0], b[1], pb[j][x][0], pb[j][x][1]);
