@@ -455,9 +455,13 @@ ra_status ring_attn_kv4_workspace_size(size_t* bytes);
  *     out = sum_c softmax_c(scale * q . k[c, h / g]) v[c, h / g]
  *     lse = ln sum_c exp(scale * q . k[c, h / g])
  * g = Hq / Hkv.  A row that sees no token gets out = 0, lse = -inf.  Rows from
- * cu[R] on are left as they are.  The results of caches that hold different parts of a
- * sequence (causal = 0 for the earlier ones) merge with ring_attn_merge,
- * which takes out as RA_FP32 and lse in this layout.
+ * cu[R] on are left as they are.  The results of caches that hold different
+ * parts of a sequence (causal = 0 for the earlier ones) merge with
+ * ring_attn_merge, which takes out as RA_FP32 and lse in this layout.
+ *
+ * Lengths and row starts outside the tensors are cut down to them, tokens of
+ * pages outside the cache are left out, and where cu falls nothing at all is
+ * computed; ring_attn_check_status reports each as RA_ERR_INVALID_ARG.
  *
  *   q        bf16 or fp16 (`dtype`) [T, Hq, d]; a token's [Hq, d] is
  *            contiguous, tokens are q_stride elements apart, a multiple of 8
@@ -472,7 +476,8 @@ ra_status ring_attn_kv4_workspace_size(size_t* bytes);
  *            the result does not need it to be tight
  *   workspace  ring_attn_kv4_workspace_size bytes                  (in/out)
  *
- * T < 2^31, Hq % Hkv == 0, W >= 1, W * page <= 2^30.  Pointers 16-byte
+ * T < 2^31, Hq % Hkv == 0, W >= 1, W * page <= 2^30; tiles of 8 rows (query
+ * tokens times g) of all requests times Hkv up to 2^24.  Pointers 16-byte
  * aligned (table, lens, cu, lse: 4).  out and lse must not overlap the inputs
  * or each other.  T == 0 or R == 0 launches nothing.
  */

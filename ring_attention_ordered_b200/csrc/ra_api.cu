@@ -845,6 +845,18 @@ ra_status ring_attn_kv4_fwd(const void* q, int64_t q_stride, const void* cache,
     return fail(RA_ERR_INVALID_ARG, "without cu every request has one query token (T=%lld R=%d)",
                 static_cast<long long>(T), R);
   if (T == 0 || R == 0) return ok();
+  // Requests of few rows go to the decoding kernel, those of many to the
+  // chunk kernel; where a batch may hold both, both are launched and each
+  // takes its own.
+  const int group = Hq / Hkv;
+  const long long rows = static_cast<long long>(cu ? (max_q < T ? max_q : T) : 1) * group;
+  const bool chunk = rows > kKv4DecodeRows, decode = !chunk || R > 1;
+  const int rows_max = chunk ? kKv4DecodeRows : 0x7fffffff;
+  if (decode && ra::kv4_decode_units(static_cast<int>(T), group, R, Hkv, rows_max) >
+                    ra::KV4_MAX_UNITS)
+    return fail(RA_ERR_UNSUPPORTED,
+                "too many requests and rows (T=%lld R=%d Hq=%d): their tiles of 8 rows times "
+                "the K/V heads must be <= 2^24", static_cast<long long>(T), R, Hq);
   if (!q || !cache || !table || !lens || !out || !lse || !workspace)
     return fail(RA_ERR_INVALID_ARG, "null pointer");
   if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || !aligned16(workspace))
@@ -869,8 +881,6 @@ ra_status ring_attn_kv4_fwd(const void* q, int64_t q_stride, const void* cache,
       if (overlaps(outs[o], out_n[o], outs[i], out_n[i]))
         return fail(RA_ERR_INVALID_ARG, "outputs and workspace overlap each other");
   }
-  int sms = 0;
-  if ((st = device_info(&sms)) != RA_OK) return st;
   ra::Kv4AttnParams prm;
   std::memset(&prm, 0, sizeof(prm));
   prm.q = q;
@@ -885,7 +895,7 @@ ra_status ring_attn_kv4_fwd(const void* q, int64_t q_stride, const void* cache,
   prm.R = R;
   prm.Hq = Hq;
   prm.Hkv = Hkv;
-  prm.group = Hq / Hkv;
+  prm.group = group;
   prm.W = W;
   prm.page = page;
   prm.num_pages = num_pages;
@@ -896,14 +906,10 @@ ra_status ring_attn_kv4_fwd(const void* q, int64_t q_stride, const void* cache,
   char* ws = static_cast<char*>(workspace);
   prm.partials = reinterpret_cast<float*>(ws + ra::KV4_COUNTER_BYTES + ra::KV4C_COUNTER_BYTES);
   prm.wait_limit_ns = g_wait_limit_ns.load();
-  // Requests of few rows go to the decoding kernel, those of many to the
-  // chunk kernel; where a batch may hold both, both are launched and each
-  // takes its own.
-  const long long rows =
-      static_cast<long long>(cu ? (max_q < prm.T ? max_q : prm.T) : 1) * prm.group;
-  const bool chunk = rows > kKv4DecodeRows, decode = !chunk || R > 1;
-  prm.rows_max = chunk ? kKv4DecodeRows : 0x7fffffff;
+  prm.rows_max = rows_max;
   prm.rows_min = decode ? kKv4DecodeRows : 0;
+  int sms = 0;
+  if ((st = device_info(&sms)) != RA_OK) return st;
   cudaError_t e = cudaSuccess;
   if (decode) {
     prm.counters = reinterpret_cast<unsigned*>(ws);

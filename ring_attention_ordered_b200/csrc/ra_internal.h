@@ -201,6 +201,14 @@ struct Kv4AttnParams {
   float* partials;        // workspace
   unsigned long long wait_limit_ns;
 };
+// No more units (a K/V head and a tile of 8 rows of a request) than this come
+// to the decoding kernel, which counts their cells in 32 bits: KV4_MAX_UNITS.
+inline double kv4_decode_units(int T, int group, int R, int Hkv, int rows_max) {
+  const double tiles = static_cast<double>(T) * group / 8 + R;
+  const double most = static_cast<double>(R) * (rows_max / 8 + 1);
+  return (tiles < most ? tiles : most) * Hkv;
+}
+constexpr double KV4_MAX_UNITS = 16777216.0;
 cudaError_t launch_kv4_plan(const Kv4PlanParams& p, cudaStream_t stream);
 cudaError_t launch_kv4_append(const Kv4CopyParams& p, int d, int dtype, cudaStream_t stream);
 cudaError_t launch_kv4_read(const Kv4CopyParams& p, int d, int dtype, cudaStream_t stream);

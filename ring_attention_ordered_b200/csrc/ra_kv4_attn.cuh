@@ -25,10 +25,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 struct Kv4Req {
   int first, n, len;
   bool bad;
+  bool falls;   // cu falls here: then the requests' rows may overlap (see kv4_load)
 };
 __device__ __forceinline__ Kv4Req kv4_request(const Kv4AttnParams& p, int r) {
   Kv4Req q;
-  q.bad = false;
+  q.bad = q.falls = false;
   int len = p.lens[r];
   const long long room = static_cast<long long>(p.W) * p.page;
   if (len < 0 || len > room) {
@@ -41,6 +42,7 @@ __device__ __forceinline__ Kv4Req kv4_request(const Kv4AttnParams& p, int r) {
     b = p.cu[r + 1];
     if (a < 0 || b < a || b > p.T) {
       q.bad = true;
+      q.falls = b < a;
       a = min(max(a, 0), p.T);
       b = min(max(b, a), p.T);
     }
@@ -205,17 +207,20 @@ struct Kv4Start {
   int r, unit, off;
 };
 
+// Where cu falls anywhere the launch does nothing: only as long as it does not,
+// the requests together have no more rows than q, which is what keeps the cells of
+// the line in 32 bits.
 struct Kv4Load {
   int units, nb;
-  bool odd;
+  bool odd, falls;
 };
 template <int ROWS>
 __device__ __forceinline__ Kv4Load kv4_load(const Kv4AttnParams& p, int r) {
-  if (r >= p.R) return {0, 0, false};
+  if (r >= p.R) return {0, 0, false, false};
   const Kv4Req q = kv4_request(p, r);
   const int nb = (q.len + KV4_BLOCK - 1) / KV4_BLOCK, rows = q.n * p.group;
   return {nb == 0 || rows > p.rows_max ? 0 : (rows + ROWS - 1) / ROWS * p.Hkv, nb,
-          q.bad || nb == 0};
+          q.bad || nb == 0, q.falls};
 }
 
 __device__ __forceinline__ int kv4_warp_scan(int x) {
@@ -281,6 +286,11 @@ __device__ __forceinline__ Kv4Start kv4_find_start(const Kv4AttnParams& p, int l
   if (p.R <= 32) {
     const Kv4Load x = kv4_load<ROWS>(p, lane);
     line.odd = __any_sync(0xffffffffu, x.odd);
+    if (line.odd && __any_sync(0xffffffffu, x.falls)) {
+      line.total = 0;
+      line.per = min_cells;
+      return {0, 0, 0};
+    }
     int all = line.cells(x.nb);
     int hi = kv4_warp_scan(x.units * all);
     line.total = __shfl_sync(0xffffffffu, hi, 31);
@@ -302,13 +312,14 @@ __device__ __forceinline__ Kv4Start kv4_find_start(const Kv4AttnParams& p, int l
   // thread tid: requests [tid * each, tid * each + each)
   const int each = (p.R + WARPS * 32 - 1) / (WARPS * 32);
   int mine = 0, units = 0, most = 0;
-  bool odd = false;
+  bool odd = false, falls = false;
   for (int i = 0; i < each; ++i) {
     const Kv4Load x = kv4_load<ROWS>(p, tid * each + i);
     mine += x.units * line.cells(x.nb);
     units += x.units;
     if (x.units) most = max(most, line.cells(x.nb) - lead);
     odd |= x.odd;
+    falls |= x.falls;
   }
   int inc = kv4_warp_scan(mine);
   units = __reduce_add_sync(0xffffffffu, units);
@@ -319,6 +330,11 @@ __device__ __forceinline__ Kv4Start kv4_find_start(const Kv4AttnParams& p, int l
     s_scan[2 * WARPS + warp] = most;
   }
   line.odd = __syncthreads_or(odd);
+  if (line.odd && __syncthreads_or(falls)) {
+    line.total = 0;
+    line.per = min_cells;
+    return {0, 0, 0};
+  }
   int lo = inc - mine;
   line.total = units = most = 0;
 #pragma unroll

@@ -15,9 +15,8 @@
 //   12-15 turn them into fp16 operand tiles (128-byte swizzle): the codes of K
 //   as they are, as subnormal fp16 numbers (one AND a pair), so S has no
 //   rounding beyond fp32; the values of V, step * code + zero rounded to fp16
-//   (half a step 2^-12 of the value, next to an output of at most that
-//   precision).  Unpacking costs each tile of 128 tokens about 230 operations
-//   a thread of the four warps, once for 256 rows.
+//   (half a step, 2^-11 of the value at most, next to an output of that
+//   precision at most).  One unpacking serves 256 rows.
 // * P = 2^(s - m + 5) in fp16.  m is a maximum of the row that is moved, and O
 //   rescaled, only when P would pass 2^15: so a tile takes one pass over S, no
 //   separate search for its maximum, and what lies up to 2^29 below the
@@ -226,12 +225,13 @@ __device__ __forceinline__ void find_start(const Kv4AttnParams& p, long long* s_
   const int each = (p.R + THREADS - 1) / THREADS;
   auto cells = [&](const Req& q) { return static_cast<long long>(q.pairs) * p.Hkv * q.room; };
   long long mine = 0;
-  bool odd = false;
+  bool odd = false, falls = false;
   for (int i = 0; i < each; ++i) {
     const int r = tid * each + i;
     if (r >= p.R) break;
     const Req q = request(p, r);
     mine += cells(q);
+    falls |= q.falls;
     odd |= q.bad || q.len == 0;
   }
   long long inc = mine;
@@ -248,6 +248,8 @@ __device__ __forceinline__ void find_start(const Kv4AttnParams& p, long long* s_
     if (w < warp) lo += s_scan[w];
     total += s_scan[w];
   }
+  // cu that falls: nothing is done
+  if (any && __syncthreads_or(falls)) total = 0;
   const long long per =
       max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(MIN_TILES));
   const long long at = per * blockIdx.x;
@@ -256,7 +258,7 @@ __device__ __forceinline__ void find_start(const Kv4AttnParams& p, long long* s_
     s_start->total = total;
     s_start->per = per;
   }
-  if (at >= lo && at < lo + mine)
+  if (at < total && at >= lo && at < lo + mine)
     for (int i = 0; i < each; ++i) {
       const long long c = cells(request(p, tid * each + i));
       if (at < lo + c) {

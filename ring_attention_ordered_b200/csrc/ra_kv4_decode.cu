@@ -12,10 +12,11 @@
 //     sum p v = sum (p vs) (codeV - 8) + sum p (vz + 8 vs)
 // * A nibble under the mask 0x000f is a subnormal fp16 number, code 2^-24,
 //   and under 0x00f0 it is code 2^-20: two codes become an operand register
-//   with one AND (and one shift for every second pair), no conversion.  The
-//   factor 16 between them is taken back in q (K: both lie in the sum over d,
-//   q there is divided by 16) and in the result (V: they are different rows
-//   of it).
+//   with one AND and a shift, no conversion.  K takes both forms (one shift for
+//   four pairs) and q is divided by 16 where the larger one meets it.  V takes
+//   all codes in the larger form: an instruction aligns its products before
+//   it adds them, and numbers that far below fp16's normal range lose places
+//   there, which over a million tokens shows (0.0019 against 0.0016, below).
 // * The 8 is taken off V's codes after the product, so that nothing is done to
 //   a single code: one more matrix instruction per block forms the sum of
 //   the rounded p vs.  Two blocks go through together, and the second enters
@@ -30,28 +31,35 @@
 //   [2^14, 2^15): exact in fp16 for bf16 and fp16 inputs down to 2^-24 of the
 //   row's maximum.
 // * p vs = 2^(s - m + 8) vs is rounded to fp16 (half a step, 2^-11 relative: no
-//   coarser than the output) for the product with the codes; the row sum and the sum of
-//   p vz use the fp32 values.  m is any reference that keeps p vs below
+//   coarser than the output) for the product with the codes; the row sum and
+//   the sum of p vz use the fp32 values.  m is any reference that keeps p vs below
 //   2^15: it is moved, and the accumulators rescaled, only when a value of the
-//   block in hand would pass that, which one vote per block finds out.  The
-//   step is part of what is bounded, so m follows max(s + log2 vs).
+//   two blocks in hand would pass that, which one vote finds out.  The step is
+//   part of what is bounded, so m follows max(s + log2 vs).
 //
 // Work: S^T = K q^T and O^T = V^T P^T with mma m16n8k16: a block of 16 tokens
 // is the M side, 8 query rows (NT tiles of them) the N side, so the padding of
 // a small group costs idle columns, not tensor time.  The transposition of P
 // between the products is one movmatrix per 8 tokens.  Each warp streams
 // pairs of blocks through a private ring of shared-memory stages (one bulk
-// copy a block; a stage is refilled as soon as its words are in registers).
+// copy for two that lie side by side: 213 us and 207 us below; a stage is refilled as
+// soon as its words are in registers).
 //
 // Split: the blocks of all (request, head, row tile) units form one line,
 // request-major, and the warps of the launch take equal stretches of it, so a
 // long request is spread over the GPU and short ones are packed, whatever the
-// lengths, which only the device knows.  A unit inside one warp's stretch is finished by
-// that warp alone, without the CTA; one that crosses warps is merged by their
-// CTA at its end, and one that crosses CTAs by the CTA that finishes last of
+// lengths, which only the device knows.  A unit inside one warp's stretch is
+// finished by that warp alone, without the CTA; one that crosses warps is merged
+// by their CTA at its end, and one that crosses CTAs by the CTA that finishes last of
 // each 16, then by the last of these (counters that they set back to zero),
 // always over the pieces in their order, so the result does not depend on the
 // order of arrival.
+//
+// What bounds it, measured: with much work the instruction issue of unpacking
+// (271 instructions a block and head, 55% of the issue slots, the ALU pipe 52%
+// busy): 8 requests of 32K tokens, 32 K/V heads, d = 128 take 207 us, 5300 GB/s
+// of cache, 0.80 of the copy rate.  With little work the chain lens, table, block, products,
+// merge: 9.4 us for one request of 509 tokens.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -68,21 +76,13 @@
 namespace ra {
 namespace kv4d {
 
-#ifndef KV4_MINC
-#define KV4_MINC 8
-#endif
-#ifndef KV4_UC
-#define KV4_UC 8
-#endif
-#ifndef KV4_WARPS
-#define KV4_WARPS 8
-#endif
-constexpr int WARPS = KV4_WARPS;
+constexpr int WARPS = 8;
 constexpr int THREADS = WARPS * 32;
-constexpr int MIN_CELLS = KV4_MINC;      // cells below which a stretch is not cut further
+constexpr int MIN_CELLS = 8;       // cells below which a stretch is not cut further
 // What a unit costs a warp beside its blocks (start, store), in blocks: it
-// takes so many cells of the line before its first block.
-constexpr int UNIT_COST = KV4_UC;
+// takes so many cells of the line before its first block (64 requests of 0 to 8191
+// tokens: 38 us with 4, 35 us with 8).
+constexpr int UNIT_COST = 8;
 constexpr int FOLD = 16;           // pieces that one CTA folds at a time
 constexpr float P_SHIFT = 8.f;     // p vs = 2^P_SHIFT at the reference
 constexpr float P_LIMIT = 32768.f;
@@ -762,7 +762,7 @@ cudaError_t launch(Kv4AttnParams p, int num_sms, int max_ctas, cudaStream_t stre
   if (grid > KV4_MAX_CTAS) grid = KV4_MAX_CTAS;
   // no more units, and with the longest requests the table can name cells,
   // than these (aligned units are padded to four times their cells at most)
-  const double units = (static_cast<double>(p.T) * p.group / S::ROWS + p.R) * p.Hkv;
+  const double units = kv4_decode_units(p.T, p.group, p.R, p.Hkv, p.rows_max);
   const double blocks = 4.0 * p.W * p.page / KV4_BLOCK;
   p.cell_shift = 0;
   while (units * (blocks / (1ll << p.cell_shift) + UNIT_COST + MIN_CELLS * WARPS) >= 2e9) ++p.cell_shift;

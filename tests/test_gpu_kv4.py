@@ -542,6 +542,38 @@ def test_pages_out_of_range_are_left_out_and_reported(ra):
         ra.check_status()
 
 
+@pytest.mark.parametrize("R,n", [(3, 2), (40, 3), (3, 200), (40, 60)])
+def test_row_starts_that_fall_are_refused(ra, R, n):
+    """Up to 32 requests and more, each kernel: no row is written, the error is
+    reported, and the next call with the workspace is right."""
+    from ring_attention_ordered_b200 import _lib
+    b = Batch(ra, [500 + n] * R, [n] * R, 8, 2, 64, 32, torch.bfloat16, 62)
+    ws = ra.kv4_workspace()
+    cu = b.cu.clone()
+    cu[1::2] = b.q.shape[0]
+    out = torch.full(b.q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full(b.q.shape[:2], 7.0, device="cuda")
+    ra.kv4_fwd(b.q.cuda(), b.cache, b.table, b.len_t, cu=cu, max_q=n, out=out, lse=lse,
+               workspace=ws)
+    with pytest.raises(_lib.RingAttnError) as e:
+        ra.check_status()
+    assert e.value.status == _lib.RA_ERR_INVALID_ARG
+    assert bool((out == 7).all()) and bool((lse == 7).all())
+    assert not bool(ws[:_lib.KV4_COUNTER_BYTES].any())
+    attend(ra, b)
+
+
+def test_a_table_far_wider_than_the_lengths(ra):
+    """2^20 columns of 1024 tokens: the line of work is then counted in groups
+    of blocks, so that its longest possible form fits 32 bits."""
+    b = Batch(ra, [4000, 17, 0, 1025, 900, 6000, 1, 300], [2] * 8, 16, 8, 64, 1024, torch.bfloat16,
+              61)
+    wide = torch.full((8, 1 << 20), -1, dtype=torch.int32, device="cuda")
+    wide[:, :b.table.shape[1]] = b.table
+    b.table = wide
+    attend(ra, b)
+
+
 def test_many_requests(ra):
     """More requests than threads, most of them short or empty."""
     r = random.Random(5)

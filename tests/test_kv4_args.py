@@ -104,7 +104,7 @@ def fwd(lib, **kw):
     (dict(ws=0), INV), (dict(wsb=100), INV), (dict(q=A[0] + 2), INV), (dict(lse=A[6] + 2), INV),
     (dict(ws=A[7] + 4), INV), (dict(out=A[0]), INV), (dict(lse=A[5] + 16), INV),
     (dict(ws=A[1]), INV), (dict(ws=A[5] + 64), INV), (dict(lse=A[3]), INV),
-    (dict(T=1 << 30, Hq=8), INV),
+    (dict(T=1 << 30, Hq=8), INV), (dict(T=1 << 23, R=1 << 23, max_q=1), UNS),
 ])
 def test_fwd_refuses(lib, kw, status):
     assert fwd(lib, **kw) == status
