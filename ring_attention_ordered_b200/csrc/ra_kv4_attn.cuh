@@ -247,7 +247,7 @@ __device__ __forceinline__ Kv4Layout kv4_layout(int units, int most, int total, 
   int per2, align;
   const int each = warps / units;           // warps a unit
   if (each < WARPS) {
-    const int a = each >= 4 && WARPS > 4 ? 4 : each >= 2 ? 2 : 1;
+    const int a = each >= 8 ? 8 : each >= 4 ? 4 : each >= 2 ? 2 : 1;
     per2 = (most + a - 1) / a;
     align = a;
   } else {
@@ -313,8 +313,11 @@ __device__ __forceinline__ Kv4Start kv4_find_start(const Kv4AttnParams& p, int l
   const int each = (p.R + WARPS * 32 - 1) / (WARPS * 32);
   int mine = 0, units = 0, most = 0;
   bool odd = false, falls = false;
+  Kv4Load only = {0, 0, false, false};   // the thread's request if it has but one
+  auto load = [&](int i) { return each == 1 ? only : kv4_load<ROWS>(p, tid * each + i); };
   for (int i = 0; i < each; ++i) {
     const Kv4Load x = kv4_load<ROWS>(p, tid * each + i);
+    only = x;
     mine += x.units * line.cells(x.nb);
     units += x.units;
     if (x.units) most = max(most, line.cells(x.nb) - lead);
@@ -348,7 +351,7 @@ __device__ __forceinline__ Kv4Start kv4_find_start(const Kv4AttnParams& p, int l
     __syncthreads();
     mine = 0;
     for (int i = 0; i < each; ++i) {
-      const Kv4Load x = kv4_load<ROWS>(p, tid * each + i);
+      const Kv4Load x = load(i);
       mine += x.units * line.cells(x.nb);
     }
     inc = kv4_warp_scan(mine);
@@ -367,7 +370,7 @@ __device__ __forceinline__ Kv4Start kv4_find_start(const Kv4AttnParams& p, int l
   int x = max((lo + line.per - 1) / line.per - me0, 0);
   if (x < WARPS && (me0 + x) * line.per < lo + mine) {
     for (int i = 0; i < each; ++i) {
-      const Kv4Load l = kv4_load<ROWS>(p, tid * each + i);
+      const Kv4Load l = load(i);
       const int all = line.cells(l.nb), hi = lo + l.units * all;
       for (; x < WARPS && (me0 + x) * line.per < hi; ++x) {
         const int in = (me0 + x) * line.per - lo, u = in / all;

@@ -76,8 +76,6 @@
 namespace ra {
 namespace kv4d {
 
-constexpr int WARPS = 8;
-constexpr int THREADS = WARPS * 32;
 constexpr int MIN_CELLS = 8;       // cells below which a stretch is not cut further
 // What a unit costs a warp beside its blocks (start, store), in blocks: it
 // takes so many cells of the line before its first block (64 requests of 0 to 8191
@@ -94,7 +92,10 @@ __device__ unsigned long long g_status = 0ull;
 template <int D, int NT>
 struct Smem {
   static constexpr int STAGES = 2;   // of two blocks each
-  static constexpr int CTAS = D * NT <= 128 ? 16 / WARPS : 8 / WARPS;   // on an SM
+  // One CTA an SM, of 16 warps if their registers allow it: two of 8 make
+  // twice as many units cross CTAs (one request of 1M tokens: 71 us against 67 us).
+  static constexpr int WARPS = D * NT <= 128 ? 16 : 8;
+  static constexpr int THREADS = WARPS * 32;
   static constexpr int WRING = STAGES * 2 * Kv4<D>::BLOCK_BYTES;
   static constexpr int ROWS = 8 * NT;
   static constexpr int RS = D + 4;                       // row stride of a piece
@@ -104,6 +105,10 @@ struct Smem {
   static constexpr int OFF_ML = OFF_HEAD + WARPS * PIECE;
   static constexpr int OFF_BAR = OFF_ML + 2 * 2 * WARPS * ROWS * 4;
   static constexpr int BYTES = OFF_BAR + WARPS * STAGES * 8;
+  // of a piece in the workspace: m and l of its rows, then the rows
+  static constexpr int SLOT = 2 * ROWS + ROWS * D;       // floats
+  static_assert(SLOT <= KV4_PIECE_FLOATS && SLOT % 4 == 0, "a piece fits its place");
+  static_assert(FOLD * SLOT * 4 <= OFF_ML, "the pieces of a fold fit the shared memory");
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -168,97 +173,107 @@ struct Group {
   int n_rows, first, h, row0, w0, w1;
 };
 
-// Pieces of unit u in the workspace, of the CTAs c0 + i step, i < n, folded in
-// that order: stored as the result, or as the piece of the first of them.
-// s_part: shared memory for [parts][items][a, m, l].
 template <int D, int NT>
-__device__ __noinline__ void kv4_fold(const Kv4AttnParams& p, const Group u, int c0, int step, int n,
-                                      bool starts, bool finish, float* s_part) {
-  constexpr int ROWS = 8 * NT, LPR = D / 4;
-  const int tid = threadIdx.x;
-  const int items = u.n_rows * LPR;
-  // Part y of the threads folds every parts-th piece of (row, 4 elements) x,
-  // with all loads of a round in flight; then the parts are merged.
-  const int parts = max(THREADS / items, 1);
-  for (int i = tid; i < items * parts; i += THREADS) {
-    const int y = i / items, x = i - y * items;
-    const int row = x / LPR, d = 4 * (x - row * LPR);
-    float m = -INFINITY, ls = 0.f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int U = 8;
+__device__ __forceinline__ float* kv4_slot(const Kv4AttnParams& p, int cta, bool starts) {
+  return p.partials + (2ll * cta + starts) * KV4_PIECE_FLOATS;
+}
+
+// Pieces of a unit in shared memory (float offsets): the i-th has its rows at
+// rows + i step, row_step apart, and m, l of row x at ml + i ml_step + 2 x; the
+// first one is at rows0 and ml0.
+struct Pieces {
+  int n, rows0, rows, step, row_step, ml0, ml, ml_step;
+};
+
+// Merges them in their order: stored as the unit's result, or, if `slot` is
+// given, as a piece there.  Every thread of the CTA takes part.  First the
+// largest m, then the sums: the loads of a few pieces are in flight together
+// (one piece after the other, running maximum: 64 requests of 0 to 8191 tokens
+// 31.6 us, so 30.8 us).
+template <int D, int NT>
+__device__ __forceinline__ void kv4_merge_pieces(const Kv4AttnParams& p, const Group& u,
+                                                 const Pieces& x, const float* smem, float* slot) {
+  constexpr int LPR = D / 4;             // lanes of a row
 #pragma unroll 1
-    for (int c = y; c < n; c += U * parts) {
-      float mm[U], ll[U];
-      float4 aa[U];
-#pragma unroll
-      for (int v = 0; v < U; ++v) {
-        const int cv = c + v * parts;
-        const float* src =
-            p.partials + (2ll * (c0 + cv * step) + (starts && cv == 0)) * KV4_PIECE_FLOATS;
-        mm[v] = -INFINITY;
-        if (cv < n) {
-          mm[v] = __ldcg(src + ROWS * D + row);
-          ll[v] = __ldcg(src + ROWS * D + ROWS + row);
-          aa[v] = __ldcg(reinterpret_cast<const float4*>(src + row * D + d));
-        }
-      }
-#pragma unroll
-      for (int v = 0; v < U; ++v)
-        if (mm[v] != -INFINITY) kv4_merge(m, ls, a, mm[v], ll[v], aa[v]);
-    }
-    float* dst = s_part + 8 * i;
-    *reinterpret_cast<float4*>(dst) = a;
-    dst[4] = m;
-    dst[5] = ls;
-  }
-  __syncthreads();   // also: every piece has been read
-  for (int i = tid; i < items; i += THREADS) {
+  for (int i = threadIdx.x; i < u.n_rows * LPR; i += Smem<D, NT>::THREADS) {
     const int row = i / LPR, d = 4 * (i - row * LPR);
+    auto ml = [&](int c) {
+      return *reinterpret_cast<const float2*>(smem + (c == 0 ? x.ml0 : x.ml + c * x.ml_step) +
+                                              2 * row);
+    };
     float m = -INFINITY, ls = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < x.n; ++c) m = fmaxf(m, ml(c).x);
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-    for (int y = 0; y < parts; ++y) {
-      const float* src = s_part + 8 * (y * items + i);
-      kv4_merge(m, ls, a, src[4], src[5], *reinterpret_cast<const float4*>(src));
+#pragma unroll 4
+    for (int c = 0; c < x.n; ++c) {
+      const float2 t = ml(c);
+      const float4 b = *reinterpret_cast<const float4*>(
+          smem + (c == 0 ? x.rows0 : x.rows + c * x.step) + row * x.row_step + d);
+      // a piece whose rows saw nothing has m = -inf and zeros
+      const float f = t.x == m ? 1.f : ex2_approx(t.x - m);
+      ls = fmaf(t.y, f, ls);
+      a.x = fmaf(b.x, f, a.x);
+      a.y = fmaf(b.y, f, a.y);
+      a.z = fmaf(b.z, f, a.z);
+      a.w = fmaf(b.w, f, a.w);
     }
-    if (finish) {
+    if (slot == nullptr) {
       kv4_store(p, u.first, u.h, u.row0 + row, d, D, a, m - P_SHIFT, ls);
     } else {
-      float* dst = p.partials + (2ll * c0 + starts) * KV4_PIECE_FLOATS;
-      *reinterpret_cast<float4*>(dst + row * D + d) = a;
-      if (d == 0) {
-        dst[ROWS * D + row] = m;
-        dst[ROWS * D + ROWS + row] = ls;
-      }
+      *reinterpret_cast<float4*>(slot + 2 * Smem<D, NT>::ROWS + row * D + d) = a;
+      if (d == 0) *reinterpret_cast<float2*>(slot + 2 * row) = make_float2(m, ls);
     }
   }
 }
 
-// Counts this CTA in at `counter`; true in all of its threads if it is the
-// last of `n`, which sets the counter back to zero.
-__device__ __forceinline__ bool kv4_last(unsigned* counter, int n, int* s_last) {
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const unsigned old = atomicAdd(counter, 1u);
-    *s_last = old == static_cast<unsigned>(n - 1);
-    if (*s_last) *counter = 0u;
-    __threadfence();
+// Pieces of unit u in the workspace, of the CTAs c0 + i step, i < n, folded in
+// that order: stored as the result, or as the piece of the first of them.
+// smem: room for the pieces.
+template <int D, int NT>
+__device__ __forceinline__ void kv4_fold(const Kv4AttnParams& p, const Group u, int c0, int step,
+                                         int n, bool starts, bool finish, float* smem) {
+  using S = Smem<D, NT>;
+  const int chunks = (2 * S::ROWS + u.n_rows * D) / 4;
+#pragma unroll 1
+  for (int c = 0; c < n; ++c) {
+    const float* src = kv4_slot<D, NT>(p, c0 + c * step, starts && c == 0);
+    const uint32_t dst = smem_u32(smem + c * S::SLOT);
+#pragma unroll 1
+    for (int i = threadIdx.x; i < chunks; i += S::THREADS)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * i), "l"(src + 4 * i)
+                   : "memory");
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  return *s_last != 0;
+  kv4_merge_pieces<D, NT>(p, u, {n, 2 * S::ROWS, 2 * S::ROWS, S::SLOT, D, 0, 0, S::SLOT}, smem,
+                          finish ? nullptr : kv4_slot<D, NT>(p, c0, starts));
+  __syncthreads();
+}
+
+// Counts this CTA, all of whose threads have passed a barrier since they wrote,
+// in at `counter`; true if it is the last of `n`, which sets the counter back
+// to zero.  By one thread.
+__device__ __forceinline__ bool kv4_last(unsigned* counter, int n) {
+  __threadfence();
+  const bool last = atomicAdd(counter, 1u) == static_cast<unsigned>(n - 1);
+  if (last) {
+    __threadfence();
+    *counter = 0u;
+  }
+  return last;
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(THREADS, (Smem<D, NT>::CTAS))
+__global__ void __launch_bounds__((Smem<D, NT>::THREADS), 1)
     ra_kv4_decode_kernel(const __grid_constant__ Kv4AttnParams p) {
   using L = Kv4<D>;
   using S = Smem<D, NT>;
   constexpr int WPL = D / 32;        // code words of a row per lane (16 or 8 bytes)
-  constexpr int ROWS = 8 * NT, STAGES = S::STAGES;
+  constexpr int ROWS = 8 * NT, STAGES = S::STAGES, WARPS = S::WARPS, THREADS = S::THREADS;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t s_abort;
-  __shared__ int s_last;
+  __shared__ bool s_last[2];
   __shared__ Kv4Start s_start[WARPS];
   __shared__ int s_scan[3 * WARPS];
   __shared__ Group s_group[WARPS + 1];   // 0: the CTA's first piece, 1 + w: warp w's tail
@@ -686,59 +701,60 @@ __global__ void __launch_bounds__(THREADS, (Smem<D, NT>::CTAS))
   const int cta0 = blockIdx.x * WARPS;
   const unsigned groups = __ballot_sync(0xffffffffu, lane <= WARPS && s_group[min(lane, WARPS)].n_rows > 0);
   unsigned crossing = 0;                 // groups that other CTAs hold pieces of
-  constexpr int LPR = D / 4;             // lanes of a row
-  constexpr int RPW = 32 / LPR;          // rows a warp takes at once
-  const int d4 = 4 * (lane % LPR);
+  float* const pieces = reinterpret_cast<float*>(smem);
 #pragma unroll 1
   for (unsigned rest = groups; rest != 0; rest &= rest - 1) {
     const int k = __ffs(rest) - 1;
     const Group u = s_group[k];
-    const int n_rows = u.n_rows;
     const int lo = max(u.w0 - cta0, 0), hi = min(u.w1 - cta0, WARPS - 1);
     const int c0 = u.w0 / WARPS, c1 = u.w1 / WARPS;
     if (c0 != c1) crossing |= 1u << k;
-    float* slot =
-        p.partials + (2ll * blockIdx.x + (static_cast<int>(blockIdx.x) == c0)) * KV4_PIECE_FLOATS;
-    for (int rb = warp * RPW; rb < n_rows; rb += WARPS * RPW) {
-      const int row = rb + lane / LPR;
-      if (row >= n_rows) continue;
-      float m = -INFINITY, ls = 0.f;
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-      for (int w = lo; w <= hi; ++w) {
-        const bool head = cta0 + w != u.w0;
-        const float* ml = s_ml + ((w * 2 + head) * ROWS + row) * 2;
-        kv4_merge(m, ls, a, ml[0], ml[1],
-                  *reinterpret_cast<const float4*>(piece_at(w, head) + row * S::RS + d4));
-      }
-      if (c0 == c1) {
-        kv4_store(p, u.first, u.h, u.row0 + row, d4, D, a, m - P_SHIFT, ls);
-      } else {
-        *reinterpret_cast<float4*>(slot + row * D + d4) = a;
-        if (d4 == 0) {
-          slot[ROWS * D + row] = m;
-          slot[ROWS * D + ROWS + row] = ls;
-        }
-      }
-    }
+    const bool head = cta0 + lo != u.w0;     // the first piece is no tail
+    const Pieces x = {hi - lo + 1,
+                      head ? S::OFF_HEAD / 4 + lo * (S::PIECE / 4) : lo * (S::WRING / 4),
+                      S::OFF_HEAD / 4 + lo * (S::PIECE / 4), S::PIECE / 4, S::RS,
+                      S::OFF_ML / 4 + (2 * lo + head) * 2 * ROWS,
+                      S::OFF_ML / 4 + (2 * lo + 1) * 2 * ROWS, 4 * ROWS};
+    kv4_merge_pieces<D, NT>(p, u, x, pieces,
+                            c0 == c1 ? nullptr
+                                     : kv4_slot<D, NT>(p, blockIdx.x,
+                                                       static_cast<int>(blockIdx.x) == c0));
   }
 
-  // ---- units that cross CTAs: the last of every FOLD of them folds their
-  // pieces, the last to do so folds these
-  float* s_part = reinterpret_cast<float*>(smem);   // the pieces there have been read
-#pragma unroll 1
-  for (; crossing != 0; crossing &= crossing - 1) {
-    const Group u = s_group[__ffs(crossing) - 1];
+  // ---- units that cross CTAs, one from before this CTA and one to behind it: the
+  // last of every FOLD of them folds their pieces, the last to do so folds these
+  if (crossing == 0) {
+    if (line.odd) kv4_fill_empty<D, THREADS>(p, &g_status);
+    return;
+  }
+  __syncthreads();   // all is written, and the pieces in shared memory have been read
+  const int k0 = __ffs(crossing) - 1, k1 = 31 - __clz(crossing);
+  if (tid < 2) {
+    const Group u = s_group[tid == 0 ? k0 : k1];
     const int c0 = u.w0 / WARPS, c1 = u.w1 / WARPS;
     const int sub = (static_cast<int>(blockIdx.x) - c0) / FOLD, first = c0 + sub * FOLD;
-    const int n = min(FOLD, c1 - first + 1);
-    const bool starts = sub == 0;
-    if (!kv4_last(p.counters + 2 * first + starts, n, &s_last)) continue;
+    s_last[tid] = (tid == 0 || k0 != k1) &&
+                  kv4_last(p.counters + 2 * first + (sub == 0), min(FOLD, c1 - first + 1));
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    if (!s_last[i]) continue;
+    const Group u = s_group[i == 0 ? k0 : k1];
+    const int c0 = u.w0 / WARPS, c1 = u.w1 / WARPS;
+    const int sub = (static_cast<int>(blockIdx.x) - c0) / FOLD, first = c0 + sub * FOLD;
     const bool one = c1 - c0 < FOLD;
-    kv4_fold<D, NT>(p, u, first, 1, n, starts, one, s_part);
     const int subs = (c1 - c0) / FOLD + 1;
-    if (one || !kv4_last(p.counters + 2 * KV4_MAX_CTAS + c0, subs, &s_last)) continue;
-    kv4_fold<D, NT>(p, u, c0, FOLD, subs, true, true, s_part);
+#pragma unroll 1
+    for (bool top = false;; top = true) {
+      kv4_fold<D, NT>(p, u, top ? c0 : first, top ? FOLD : 1,
+                      top ? subs : min(FOLD, c1 - first + 1), top || sub == 0, top || one, pieces);
+      if (one || top) break;
+      // s_last[i] has been read by all: the fold has barriers
+      if (tid == 0) s_last[i] = kv4_last(p.counters + 2 * KV4_MAX_CTAS + c0, subs);
+      __syncthreads();
+      if (!s_last[i]) break;
+    }
   }
   if (line.odd) kv4_fill_empty<D, THREADS>(p, &g_status);
 }
@@ -757,7 +773,7 @@ cudaError_t launch(Kv4AttnParams p, int num_sms, int max_ctas, cudaStream_t stre
     if (e != cudaSuccess) return e;
     configured_dev[dev] = 1;
   }
-  int grid = num_sms * S::CTAS;
+  int grid = num_sms;
   if (max_ctas > 0 && max_ctas < grid) grid = max_ctas;
   if (grid > KV4_MAX_CTAS) grid = KV4_MAX_CTAS;
   // no more units, and with the longest requests the table can name cells,
@@ -765,8 +781,8 @@ cudaError_t launch(Kv4AttnParams p, int num_sms, int max_ctas, cudaStream_t stre
   const double units = kv4_decode_units(p.T, p.group, p.R, p.Hkv, p.rows_max);
   const double blocks = 4.0 * p.W * p.page / KV4_BLOCK;
   p.cell_shift = 0;
-  while (units * (blocks / (1ll << p.cell_shift) + UNIT_COST + MIN_CELLS * WARPS) >= 2e9) ++p.cell_shift;
-  ra_kv4_decode_kernel<D, NT><<<grid, THREADS, S::BYTES, stream>>>(p);
+  while (units * (blocks / (1ll << p.cell_shift) + UNIT_COST + MIN_CELLS * S::WARPS) >= 2e9) ++p.cell_shift;
+  ra_kv4_decode_kernel<D, NT><<<grid, S::THREADS, S::BYTES, stream>>>(p);
   return cudaGetLastError();
 }
 
