@@ -76,7 +76,7 @@
 namespace ra {
 namespace kv4d {
 
-constexpr int MIN_CELLS = 8;       // cells below which a stretch is not cut further
+constexpr int MIN_CELLS = 4;       // cells below which a stretch is not cut further
 // What a unit costs a warp beside its blocks (start, store), in blocks: it
 // takes so many cells of the line before its first block (64 requests of 0 to 8191
 // tokens: 38 us with 4, 35 us with 8).
@@ -185,45 +185,41 @@ struct Pieces {
   int n, rows0, rows, step, row_step, ml0, ml, ml_step;
 };
 
-// Merges them in their order: stored as the unit's result, or, if `slot` is
-// given, as a piece there.  Every thread of the CTA takes part.  First the
-// largest m, then the sums: the loads of a few pieces are in flight together
-// (one piece after the other, running maximum: 64 requests of 0 to 8191 tokens
-// 31.6 us, so 30.8 us).
+// Merges elements d .. d + 3 of their row `row`, in their order: stored as the
+// unit's result, or, if `slot` is given, as a piece there.  First the largest m,
+// then the sums: the loads of a few pieces are in flight together (one piece
+// after the other, running maximum: 64 requests of 0 to 8191 tokens 31.6 us, so
+// 30.8 us).
 template <int D, int NT>
-__device__ __forceinline__ void kv4_merge_pieces(const Kv4AttnParams& p, const Group& u,
-                                                 const Pieces& x, const float* smem, float* slot) {
-  constexpr int LPR = D / 4;             // lanes of a row
-#pragma unroll 1
-  for (int i = threadIdx.x; i < u.n_rows * LPR; i += Smem<D, NT>::THREADS) {
-    const int row = i / LPR, d = 4 * (i - row * LPR);
-    auto ml = [&](int c) {
-      return *reinterpret_cast<const float2*>(smem + (c == 0 ? x.ml0 : x.ml + c * x.ml_step) +
-                                              2 * row);
-    };
-    float m = -INFINITY, ls = 0.f;
+__device__ __forceinline__ void kv4_merge_row(const Kv4AttnParams& p, const Group& u,
+                                              const Pieces& x, int row, int d, const float* smem,
+                                              float* slot) {
+  auto ml = [&](int c) {
+    return *reinterpret_cast<const float2*>(smem + (c == 0 ? x.ml0 : x.ml + c * x.ml_step) +
+                                            2 * row);
+  };
+  float m = -INFINITY, ls = 0.f;
 #pragma unroll 4
-    for (int c = 0; c < x.n; ++c) m = fmaxf(m, ml(c).x);
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = 0; c < x.n; ++c) m = fmaxf(m, ml(c).x);
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int c = 0; c < x.n; ++c) {
-      const float2 t = ml(c);
-      const float4 b = *reinterpret_cast<const float4*>(
-          smem + (c == 0 ? x.rows0 : x.rows + c * x.step) + row * x.row_step + d);
-      // a piece whose rows saw nothing has m = -inf and zeros
-      const float f = t.x == m ? 1.f : ex2_approx(t.x - m);
-      ls = fmaf(t.y, f, ls);
-      a.x = fmaf(b.x, f, a.x);
-      a.y = fmaf(b.y, f, a.y);
-      a.z = fmaf(b.z, f, a.z);
-      a.w = fmaf(b.w, f, a.w);
-    }
-    if (slot == nullptr) {
-      kv4_store(p, u.first, u.h, u.row0 + row, d, D, a, m - P_SHIFT, ls);
-    } else {
-      *reinterpret_cast<float4*>(slot + 2 * Smem<D, NT>::ROWS + row * D + d) = a;
-      if (d == 0) *reinterpret_cast<float2*>(slot + 2 * row) = make_float2(m, ls);
-    }
+  for (int c = 0; c < x.n; ++c) {
+    const float2 t = ml(c);
+    const float4 b = *reinterpret_cast<const float4*>(
+        smem + (c == 0 ? x.rows0 : x.rows + c * x.step) + row * x.row_step + d);
+    // a piece whose row saw nothing has m = -inf and zeros
+    const float f = t.x == m ? 1.f : ex2_approx(t.x - m);
+    ls = fmaf(t.y, f, ls);
+    a.x = fmaf(b.x, f, a.x);
+    a.y = fmaf(b.y, f, a.y);
+    a.z = fmaf(b.z, f, a.z);
+    a.w = fmaf(b.w, f, a.w);
+  }
+  if (slot == nullptr) {
+    kv4_store(p, u.first, u.h, u.row0 + row, d, D, a, m - P_SHIFT, ls);
+  } else {
+    *reinterpret_cast<float4*>(slot + 2 * Smem<D, NT>::ROWS + row * D + d) = a;
+    if (d == 0) *reinterpret_cast<float2*>(slot + 2 * row) = make_float2(m, ls);
   }
 }
 
@@ -246,8 +242,12 @@ __device__ __forceinline__ void kv4_fold(const Kv4AttnParams& p, const Group u, 
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  kv4_merge_pieces<D, NT>(p, u, {n, 2 * S::ROWS, 2 * S::ROWS, S::SLOT, D, 0, 0, S::SLOT}, smem,
-                          finish ? nullptr : kv4_slot<D, NT>(p, c0, starts));
+  const Pieces x = {n, 2 * S::ROWS, 2 * S::ROWS, S::SLOT, D, 0, 0, S::SLOT};
+  float* slot = finish ? nullptr : kv4_slot<D, NT>(p, c0, starts);
+  constexpr int LPR = D / 4;             // lanes of a row
+#pragma unroll 1
+  for (int i = threadIdx.x; i < u.n_rows * LPR; i += S::THREADS)
+    kv4_merge_row<D, NT>(p, u, x, i / LPR, 4 * (i % LPR), smem, slot);
   __syncthreads();
 }
 
@@ -695,30 +695,42 @@ __global__ void __launch_bounds__((Smem<D, NT>::THREADS), 1)
       s_group[head ? 0 : 1 + warp] = {min(ROWS, rows - row0), q.first, h, row0, first / per, last / per};
   }
 
-  // ---- units that cross warps: merged by the CTA, a row to a warp at a time
+  // ---- units that cross warps: merged by the CTA, their rows dealt over its
+  // threads
   __syncthreads();
   if (s_abort) return;
   const int cta0 = blockIdx.x * WARPS;
-  const unsigned groups = __ballot_sync(0xffffffffu, lane <= WARPS && s_group[min(lane, WARPS)].n_rows > 0);
-  unsigned crossing = 0;                 // groups that other CTAs hold pieces of
+  const bool any = lane <= WARPS && s_group[min(lane, WARPS)].n_rows > 0;
+  const unsigned groups = __ballot_sync(0xffffffffu, any);
+  // those of which other CTAs hold pieces
+  const unsigned crossing = __ballot_sync(
+      0xffffffffu, any && s_group[lane].w0 / WARPS != s_group[lane].w1 / WARPS);
   float* const pieces = reinterpret_cast<float*>(smem);
+  constexpr int LPR = D / 4;             // lanes of a row
+  int base = 0;                          // rows of the groups before
 #pragma unroll 1
   for (unsigned rest = groups; rest != 0; rest &= rest - 1) {
     const int k = __ffs(rest) - 1;
     const Group u = s_group[k];
+    // this thread's first row of the group
+    int row = (tid / LPR - base) % (THREADS / LPR);
+    if (row < 0) row += THREADS / LPR;
+    base += u.n_rows;
+    if (row >= u.n_rows) continue;
     const int lo = max(u.w0 - cta0, 0), hi = min(u.w1 - cta0, WARPS - 1);
-    const int c0 = u.w0 / WARPS, c1 = u.w1 / WARPS;
-    if (c0 != c1) crossing |= 1u << k;
     const bool head = cta0 + lo != u.w0;     // the first piece is no tail
     const Pieces x = {hi - lo + 1,
                       head ? S::OFF_HEAD / 4 + lo * (S::PIECE / 4) : lo * (S::WRING / 4),
                       S::OFF_HEAD / 4 + lo * (S::PIECE / 4), S::PIECE / 4, S::RS,
                       S::OFF_ML / 4 + (2 * lo + head) * 2 * ROWS,
                       S::OFF_ML / 4 + (2 * lo + 1) * 2 * ROWS, 4 * ROWS};
-    kv4_merge_pieces<D, NT>(p, u, x, pieces,
-                            c0 == c1 ? nullptr
-                                     : kv4_slot<D, NT>(p, blockIdx.x,
-                                                       static_cast<int>(blockIdx.x) == c0));
+    float* slot = (crossing >> k) & 1u
+                      ? kv4_slot<D, NT>(p, blockIdx.x,
+                                        static_cast<int>(blockIdx.x) == u.w0 / WARPS)
+                      : nullptr;
+#pragma unroll 1
+    for (; row < u.n_rows; row += THREADS / LPR)
+      kv4_merge_row<D, NT>(p, u, x, row, 4 * (tid % LPR), pieces, slot);
   }
 
   // ---- units that cross CTAs, one from before this CTA and one to behind it: the
