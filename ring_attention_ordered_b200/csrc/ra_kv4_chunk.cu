@@ -681,88 +681,127 @@ struct RowSync {
 
 // Pieces of a unit in the workspace, of the CTAs c0 + i step, i < n, folded in
 // that order: stored as the result, or as the piece of the first of them.  By
-// the softmax threads, a row to D / 4 lanes; each thread has 8 rows of two
-// pieces in flight.  Returns the barrier's phase, or -1 if the kernel is
-// aborting.  A function of its own, with the piece in shared memory, so that
-// the loop over the tiles keeps its registers.
+// the softmax threads: first a thread for each row, which finds the factors of
+// the row's pieces, in `tab` (shared memory, [piece][row]); then a row to D / 4
+// lanes, each thread with 8 rows in flight.  False if the kernel is aborting.
 template <int D>
-__device__ __noinline__ int fold(const Kv4AttnParams& p, const Piece* piece, int c0, int step,
-                                 int n, bool starts, bool finish, RowSync sync, Ctl cx) {
+__device__ __forceinline__ bool fold(const Kv4AttnParams& p, const Piece& x, int c0, int step,
+                                     int n, bool starts, bool finish, float* tab, RowSync& sync,
+                                     const Ctl& cx) {
   constexpr int LPR = D / 4, RPR = 256 / LPR, V = 8;   // rows a round, rows a thread
-  const Piece x = *piece;
+  // pieces in flight (d = 128: 549 us with 1, 553 with 2, two chunks of 1024 over 16K;
+  // d = 64: 93 us and 88 us, 8 chunks of 200 over 3K)
+  constexpr int E = D == 128 ? 1 : 2;
   const int rows = min(UNIT_ROWS, x.rows - x.row0);
+  const float* first = p.partials + (2ll * c0 + starts) * KV4C_PIECE_FLOATS;
+  auto piece_at = [&](int c) {
+    return c == 0 ? first : p.partials + 2ll * (c0 + c * step) * KV4C_PIECE_FLOATS;
+  };
+  auto row_at = [&](int row) {     // of the row's first element in out
+    const int tok = (x.row0 + row) / p.group;
+    return (static_cast<long long>(x.first) + tok) * p.Hq + x.h * p.group +
+           (x.row0 + row - tok * p.group);
+  };
+  const int mine = threadIdx.x;
+  if (mine < rows) {
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < n; ++c) {
+      const float mc = __ldcg(piece_at(c) + UNIT_ROWS * D + mine);
+      tab[c * UNIT_ROWS + mine] = mc;
+      m = fmaxf(m, mc);
+    }
+#pragma unroll 4
+    for (int c = 0; c < n; ++c) {
+      // a piece whose row saw nothing has m = -inf and zeros
+      const float mc = tab[c * UNIT_ROWS + mine], f = mc == m ? 1.f : ex2_approx(mc - m);
+      tab[c * UNIT_ROWS + mine] = f;
+      l = fmaf(__ldcg(piece_at(c) + UNIT_ROWS * D + UNIT_ROWS + mine), f, l);
+    }
+    if (finish) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      for (int c = 0; c < n; ++c) tab[c * UNIT_ROWS + mine] *= inv;
+      p.lse[row_at(mine)] =
+          l == 0.f ? -INFINITY : (m - P_SHIFT + log2f(l)) * 0.69314718055994530942f;
+    } else {
+      float* dst = p.partials + (2ll * c0 + starts) * KV4C_PIECE_FLOATS + UNIT_ROWS * D + mine;
+      dst[0] = m;
+      dst[UNIT_ROWS] = l;
+    }
+  }
+  if (!sync(cx)) return false;
   const int d = 4 * (threadIdx.x % LPR);
 #pragma unroll 1
   for (int rb = 0; rb < rows; rb += RPR * V) {
     const int r0 = rb + threadIdx.x / LPR;
-    float m[V], ls[V];
     float4 a[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      m[v] = -INFINITY;
-      ls[v] = 0.f;
-      a[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+    for (int v = 0; v < V; ++v) a[v] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int c = 0; c < n; ++c) {
-      const float* src =
-          p.partials + (2ll * (c0 + c * step) + (starts && c == 0)) * KV4C_PIECE_FLOATS;
-      float mm[V], ll[V];
-      float4 aa[V];
+    for (int c = 0; c < n; c += E) {
+      float4 b[E][V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int row = r0 + v * RPR;
-        mm[v] = -INFINITY;
-        if (row < rows) {
-          mm[v] = __ldcg(src + UNIT_ROWS * D + row);
-          ll[v] = __ldcg(src + UNIT_ROWS * D + UNIT_ROWS + row);
-          aa[v] = __ldcg(reinterpret_cast<const float4*>(src + row * D + d));
-        }
+      for (int e = 0; e < E; ++e) {
+        const float* src = piece_at(min(c + e, n - 1)) + r0 * D + d;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (r0 + v * RPR < rows)
+            b[e][v] = __ldcg(reinterpret_cast<const float4*>(src + v * RPR * D));
       }
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (mm[v] != -INFINITY) kv4_merge(m[v], ls[v], a[v], mm[v], ll[v], aa[v]);
+      for (int e = 0; e < E; ++e) {
+        if (c + e >= n) break;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if (r0 + v * RPR >= rows) continue;
+          const float f = tab[(c + e) * UNIT_ROWS + r0 + v * RPR];
+          a[v].x = fmaf(b[e][v].x, f, a[v].x);
+          a[v].y = fmaf(b[e][v].y, f, a[v].y);
+          a[v].z = fmaf(b[e][v].z, f, a[v].z);
+          a[v].w = fmaf(b[e][v].w, f, a[v].w);
+        }
+      }
     }
-    if (!finish && !sync(cx)) return -1;   // the round's rows have been read
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int row = r0 + v * RPR;
       if (row >= rows) continue;
-      if (finish) {
-        kv4_store(p, x.first, x.h, x.row0 + row, d, D, a[v], m[v] - P_SHIFT, ls[v]);
-      } else {
-        float* dst = p.partials + (2ll * c0 + starts) * KV4C_PIECE_FLOATS;
-        *reinterpret_cast<float4*>(dst + row * D + d) = a[v];
-        if (d == 0) {
-          dst[UNIT_ROWS * D + row] = m[v];
-          dst[UNIT_ROWS * D + UNIT_ROWS + row] = ls[v];
-        }
+      if (!finish) {
+        // this thread alone reads and writes these elements
+        *reinterpret_cast<float4*>(const_cast<float*>(first) + row * D + d) = a[v];
+        continue;
       }
+      const long long o = row_at(row) * D + d;
+      if (p.out_f32)
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) = a[v];
+      else if (p.q_f16)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o) =
+            make_uint2(pack_f16x2(a[v].x, a[v].y), pack_f16x2(a[v].z, a[v].w));
+      else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o) =
+            make_uint2(pack_bf16x2(a[v].x, a[v].y), pack_bf16x2(a[v].z, a[v].w));
     }
   }
-  return static_cast<int>(sync.phase);
+  return sync(cx);   // the table has been read
 }
 
-// Counts the CTA in at `counter`: 1 if it is the last of `n` (the counter is
-// then zero again), 0 if not, -1 if the kernel is aborting.
-__device__ __forceinline__ int count_in(unsigned* counter, int n, volatile int* s_last,
-                                        RowSync& sync, const Ctl& cx) {
+// Counts the CTA, all of whose softmax threads have passed a barrier since they
+// wrote, in at `counter`; true if it is the last of `n`, which sets the counter
+// back to zero.  By one thread.
+__device__ __forceinline__ bool count_in(unsigned* counter, int n) {
   __threadfence();
-  if (!sync(cx)) return -1;
-  if (threadIdx.x == 0) {
-    const unsigned old = atomicAdd(counter, 1u);
-    *s_last = old == static_cast<unsigned>(n - 1);
-    if (*s_last) *counter = 0u;
+  const bool last = atomicAdd(counter, 1u) == static_cast<unsigned>(n - 1);
+  if (last) {
     __threadfence();
+    *counter = 0u;
   }
-  if (!sync(cx)) return -1;
-  return *s_last;
+  return last;
 }
 
 template <int D>
 __device__ void softmax_role(const Kv4AttnParams& p, const Bars& br, uint32_t base, uint32_t tmem,
-                             int w, Piece* pieces, volatile uint32_t* held, volatile int* s_last,
-                             const Ctl& cx) {
+                             int w, Piece* pieces, volatile uint32_t* held, Piece* cut,
+                             volatile int* s_last, const Ctl& cx) {
   using C = Cfg<D>;
   const int t = threadIdx.x - w * 128;            // row inside the tile
   const int quarter = (threadIdx.x >> 5) & 3;
@@ -771,6 +810,7 @@ __device__ void softmax_role(const Kv4AttnParams& p, const Bars& br, uint32_t ba
   const uint32_t tO = tmem + lane_off + 256 + w * 128;
   uint32_t s_phase = 0u, units_w = 0u, q_uses = 0u, tile = 0u;
   RowSync sync{br.rows, 0u};
+  int n_cut = 0;      // pieces that are not whole units
 
   for (int k = 0;; ++k) {
     int u;
@@ -986,26 +1026,45 @@ __device__ void softmax_role(const Kv4AttnParams& p, const Bars& br, uint32_t ba
       ++units_w;
     }
     if (!pieces[u].whole) {
-      const int c0 = pieces[u].c0, c1 = pieces[u].c1;
-      const int sub = (static_cast<int>(blockIdx.x) - c0) / FOLD, first = c0 + sub * FOLD;
-      const int n = min(FOLD, c1 - first + 1);
-      const bool starts = sub == 0, one = c1 - c0 < FOLD;
-      int last = count_in(p.counters + 2 * first + starts, n, s_last, sync, cx);
-      if (last > 0) {
-        int ph = fold<D>(p, pieces + u, first, 1, n, starts, one, sync, cx);
-        if (ph < 0) return;
-        sync.phase = ph;
-        if (!one) {
-          const int subs = (c1 - c0) / FOLD + 1;
-          last = count_in(p.counters + 2 * KV4C_MAX_CTAS + c0, subs, s_last, sync, cx);
-          if (last > 0) ph = fold<D>(p, pieces + u, c0, FOLD, subs, true, true, sync, cx);
-          if (ph < 0) return;
-          sync.phase = last > 0 ? ph : sync.phase;
-        }
+      if (!sync(cx)) return;
+      if (threadIdx.x == 0) {
+        const int c0 = pieces[u].c0, sub = (static_cast<int>(blockIdx.x) - c0) / FOLD;
+        const int first = c0 + sub * FOLD;
+        cut[n_cut] = pieces[u];
+        s_last[n_cut] = count_in(p.counters + 2 * first + (sub == 0),
+                                 min(FOLD, pieces[u].c1 - first + 1));
       }
-      if (last < 0) return;
+      ++n_cut;
     }
     mbar_arrive(br.unit_done);
+  }
+
+  // ---- units that cross CTAs, one from before this CTA and one to behind it: the
+  // last of every FOLD of them folds their pieces, the last to do so folds these.
+  // They are counted as they are done, so that it is mostly the second that this
+  // CTA is the last for, and folded at the end: amid the tiles the fold's registers
+  // are theirs (two chunks of 1024 tokens over 16K: 573 us, so 549 us).
+  if (n_cut == 0 || !sync(cx)) return;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];   // q is no longer needed
+  float* tab = reinterpret_cast<float*>(smem_raw + (base + C::OFF_Q - smem_u32(smem_raw)));
+#pragma unroll 1
+  for (int i = 0; i < n_cut; ++i) {
+    if (!s_last[i]) continue;
+    const Piece x = cut[i];
+    const int sub = (static_cast<int>(blockIdx.x) - x.c0) / FOLD, first = x.c0 + sub * FOLD;
+    const int n = min(FOLD, x.c1 - first + 1), subs = (x.c1 - x.c0) / FOLD + 1;
+    const bool one = subs == 1;
+#pragma unroll 1
+    for (bool top = false;; top = true) {
+      if (!fold<D>(p, x, top ? x.c0 : first, top ? FOLD : 1, top ? subs : n, top || sub == 0,
+                   top || one, tab, sync, cx))
+        return;
+      if (top || one) break;
+      if (threadIdx.x == 0)
+        s_last[i] = count_in(p.counters + 2 * KV4C_MAX_CTAS + x.c0, subs);
+      if (!sync(cx)) return;
+      if (!s_last[i]) break;
+    }
   }
 }
 
@@ -1019,7 +1078,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   __shared__ uint32_t held_[NRAW + NPAR];   // blocks that a raw stage, a tile's slot holds
   __shared__ Start s_start;
   __shared__ long long s_scan[THREADS / 32];
-  __shared__ int s_odd, s_last;
+  __shared__ Piece s_cut[2];
+  __shared__ int s_odd, s_last[2];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* base_ptr = smem_raw + (base - raw);
@@ -1048,7 +1108,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
-    softmax_role<D>(p, br, base, tmem, warp >> 2, pieces, held, &s_last, cx);
+    softmax_role<D>(p, br, base, tmem, warp >> 2, pieces, held, s_cut, s_last, cx);
   } else if (warp < WARP_UNPACK) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CONTROL_REGS));
     if (warp == WARP_LOAD)
