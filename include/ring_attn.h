@@ -460,7 +460,7 @@ ra_status ring_attn_kv4_workspace_size(size_t* bytes);
  * ring_attn_merge, which takes out as RA_FP32 and lse in this layout.
  *
  * Lengths and row starts outside the tensors are cut down to them, tokens of
- * pages outside the cache are left out, and where cu falls nothing at all is
+ * pages outside the cache are left out, and where cu falls no attention is
  * computed; ring_attn_check_status reports each as RA_ERR_INVALID_ARG.
  *
  *   q        bf16 or fp16 (`dtype`) [T, Hq, d]; a token's [Hq, d] is

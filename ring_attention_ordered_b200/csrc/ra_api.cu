@@ -33,7 +33,11 @@ std::atomic<int> g_schedule{RA_SCHEDULE_AUTO};
 constexpr double kHeadMajorKvBytes = 96.0 * 1024 * 1024;
 
 // Rows (query tokens times the group's query heads) of a request up to which
-// the decoding kernel serves it.
+// the decoding kernel serves it.  The lengths, which say how much work there is,
+// are known to the device alone; the more there is, the earlier the chunk kernel
+// wins.  Measured, decoding and chunk kernel, 128 rows, 2 K/V heads: 4 requests
+// of 4000 tokens 23 us and 45 us (d = 128), 16 of 8000 94 us and 88 us (d = 128),
+// 63 us and 75 us (d = 64), 64 of 2000 104 us and 65 us (d = 128).
 constexpr int kKv4DecodeRows = 128;
 
 constexpr int kMaxDevices = 64;

@@ -185,10 +185,10 @@ __device__ __noinline__ void kv4_fill_empty(const Kv4AttnParams& p, unsigned lon
 // the lengths; but units then cross warps and CTAs where it happens.  Aligned
 // (lead 0): every unit starts at a multiple of `align` cells, the stretches of
 // 1, 2, 4 or 8 warps, so that it stays in those, or, being longer, in whole CTAs.
-// Chosen where the longest stretch grows by 6 cells and a 32nd at most: that is
-// about what pieces that cross CTAs cost (measured: 296 units of 256 blocks 49 us
-// packed, 39 us aligned; 256 units of 2000 blocks 193 us packed, 218 us aligned,
-// a stretch longer by 15%).
+// Chosen where the longest stretch grows by 3 cells and a 32nd at most: that is
+// about what pieces that cross CTAs cost (measured: 64 units of 512 blocks 27.7 us
+// packed, 25.5 us aligned; 128 units of 300 blocks 31.0 us packed, 33.5 us aligned
+// with stretches 12 cells longer).
 //
 // Cell numbers are 32 bits wide: the host chooses `shift` so that the longest
 // line the arguments allow stays below 2^31.
@@ -258,7 +258,7 @@ __device__ __forceinline__ Kv4Layout kv4_layout(int units, int most, int total, 
     align = WARPS;
   }
   per2 = max(per2, min_cells);
-  if (per2 > per + per / 32 + 6) return {per, 0};
+  if (per2 > per + per / 32 + 3) return {per, 0};
   return {per2, align * per2};
 }
 

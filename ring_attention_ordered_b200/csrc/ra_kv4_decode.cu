@@ -42,8 +42,8 @@
 // a small group costs idle columns, not tensor time.  The transposition of P
 // between the products is one movmatrix per 8 tokens.  Each warp streams
 // pairs of blocks through a private ring of shared-memory stages (one bulk
-// copy for two that lie side by side: 213 us and 207 us below; a stage is refilled as
-// soon as its words are in registers).
+// copy for two that lie side by side, 3% less than one for each; a stage is
+// refilled as soon as its words are in registers).
 //
 // Split: the blocks of all (request, head, row tile) units form one line,
 // request-major, and the warps of the launch take equal stretches of it, so a
@@ -57,9 +57,9 @@
 //
 // What bounds it, measured: with much work the instruction issue of unpacking
 // (271 instructions a block and head, 55% of the issue slots, the ALU pipe 52%
-// busy): 8 requests of 32K tokens, 32 K/V heads, d = 128 take 207 us, 5300 GB/s
-// of cache, 0.80 of the copy rate.  With little work the chain lens, table, block, products,
-// merge: 9.4 us for one request of 509 tokens.
+// busy): 8 requests of 32K tokens, 32 K/V heads, d = 128 take 191 us, 5700 GB/s
+// of cache, 0.87 of the copy rate.  With little work the chain lens, table, block,
+// products, merge: 8.8 us for one request of 509 tokens.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -76,10 +76,13 @@
 namespace ra {
 namespace kv4d {
 
-constexpr int MIN_CELLS = 4;       // cells below which a stretch is not cut further
+// Cells below which a stretch is not cut further (one request of 509 tokens: 9.3 us
+// with 2, 8.9 us with 4, 9.8 us with 8).
+constexpr int MIN_CELLS = 4;
 // What a unit costs a warp beside its blocks (start, store), in blocks: it
 // takes so many cells of the line before its first block (64 requests of 0 to 8191
-// tokens: 38 us with 4, 35 us with 8).
+// tokens: 36.8 us with 4, 30.9 us with 8, 31.4 us with 12; 8 of 32K tokens and 32
+// heads: 193 us with 4, 191 us with 8, 195 us with 16).
 constexpr int UNIT_COST = 8;
 constexpr int FOLD = 16;           // pieces that one CTA folds at a time
 constexpr float P_SHIFT = 8.f;     // p vs = 2^P_SHIFT at the reference
