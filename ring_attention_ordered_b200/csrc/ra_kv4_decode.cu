@@ -57,9 +57,9 @@
 //
 // What bounds it, measured: with much work the instruction issue of unpacking
 // (271 instructions a block and head, 55% of the issue slots, the ALU pipe 52%
-// busy): 8 requests of 32K tokens, 32 K/V heads, d = 128 take 191 us, 5700 GB/s
-// of cache, 0.87 of the copy rate.  With little work the chain lens, table, block,
-// products, merge: 8.8 us for one request of 509 tokens.
+// busy): 8 requests of 32K tokens, 32 K/V heads, d = 128 take 193 us, 5670 GB/s
+// of cache, 0.86 of the copy rate.  With little work the chain lens, table, block,
+// products, merge: 8.9 us for one request of 509 tokens.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -563,6 +563,15 @@ def test_row_starts_that_fall_are_refused(ra, R, n):
     attend(ra, b)
 
 
+@pytest.mark.parametrize("R", [31, 32, 33, 63, 64, 65])
+def test_batches_around_the_ways_to_divide_them(ra, R):
+    """Empty requests, short ones and a long one, in and out of step with the
+    requests a lane takes."""
+    lens = [(0, 40, 1, 700, 16, 17)[(r * 5 + R) % 6] for r in range(R)]
+    lens[R // 2], lens[-1] = 9001, 33
+    attend(ra, Batch(ra, lens, [1 + r % 3 for r in range(R)], 4, 2, 64, 32, torch.bfloat16, 63 + R))
+
+
 def test_a_table_far_wider_than_the_lengths(ra):
     """2^20 columns of 1024 tokens: the line of work is then counted in groups
     of blocks, so that its longest possible form fits 32 bits."""
