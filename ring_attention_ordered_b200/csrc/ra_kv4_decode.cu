@@ -458,7 +458,7 @@ __global__ void __launch_bounds__((Smem<D, NT>::THREADS), 1)
     }
 
     // One pair of blocks.  TAIL: some of its tokens are hidden from some row.
-      auto step = [&](auto tail_c, int i) {
+    auto step = [&](auto tail_c, int i) {
       constexpr bool TAIL = decltype(tail_c)::value;
       const uint32_t s = (it0 + i) % STAGES;
       const uint32_t held = (have >> (2 * s)) & 3u;
@@ -694,7 +694,7 @@ __global__ void __launch_bounds__((Smem<D, NT>::THREADS), 1)
           ml[2 * row + 1] = l[j][cc];
         }
       }
-    if (lane == 0 && (!head || warp == 0)) 
+    if (lane == 0 && (!head || warp == 0))
       s_group[head ? 0 : 1 + warp] = {min(ROWS, rows - row0), q.first, h, row0, first / per, last / per};
   }
 
