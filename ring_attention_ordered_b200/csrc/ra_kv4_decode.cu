@@ -10,13 +10,15 @@
 // zeros are applied in fp32 around them, so nothing of K or V is rounded:
 //     q . k   = ks (q . codeK) + kz sum(q)
 //     sum p v = sum (p vs) (codeV - 8) + sum p (vz + 8 vs)
-// * A nibble under the mask 0x000f is a subnormal fp16 number, code 2^-24,
-//   and under 0x00f0 it is code 2^-20: two codes become an operand register
-//   with one AND and a shift, no conversion.  K takes both forms (one shift for
-//   four pairs) and q is divided by 16 where the larger one meets it.  V takes
-//   all codes in the larger form: an instruction aligns its products before
-//   it adds them, and numbers that far below fp16's normal range lose places
-//   there, which over a million tokens shows (0.0019 against 0.0016, below).
+// * A nibble under a mask is a subnormal fp16 number, code 2^-24 under 0x000f, or a
+//   power of two times that after a shift: two codes become an operand register with
+//   one AND and a shift, no conversion.  An instruction aligns its products before
+//   it adds them, and numbers far below fp16's normal range lose places there.
+//   So K's codes enter as code 2^-22 and code 2^-18 (one shift for two pairs; q is
+//   divided by 16 where it meets the larger ones): with 2^-24 and 2^-20, half a shift
+//   less, lse was up to 1.1e-5 off for fp16 q and short requests, 3e-6 so (193 us and
+//   196 us below; all at 2^-20, a shift more, 202 us).  V takes all codes at 2^-20, which over a million tokens
+//   shows (0.0016 off, below, and 0.0019 with 2^-24).
 // * The 8 is taken off V's codes after the product, so that nothing is done to
 //   a single code: one more matrix instruction per block forms the sum of
 //   the rounded p vs.  Two blocks go through together, and the second enters
@@ -57,9 +59,9 @@
 //
 // What bounds it, measured: with much work the instruction issue of unpacking
 // (271 instructions a block and head, 55% of the issue slots, the ALU pipe 52%
-// busy): 8 requests of 32K tokens, 32 K/V heads, d = 128 take 193 us, 5670 GB/s
-// of cache, 0.86 of the copy rate.  With little work the chain lens, table, block,
-// products, merge: 8.9 us for one request of 509 tokens.
+// busy): 8 requests of 32K tokens, 32 K/V heads, d = 128 take 196 us, 5570 GB/s
+// of cache, 0.85 of the copy rate.  With little work the chain lens, table, block,
+// products, merge: 8.8 us for one request of 509 tokens.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -151,13 +153,13 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   return r;
 }
 // Nibbles (0, 4), (1, 5), (2, 6), (3, 7) of a word as fp16 pairs: codes times
-// 2^-24, 2^-20, 2^-24, 2^-20.
+// 2^-22, 2^-18, 2^-22, 2^-18.
 __device__ __forceinline__ void code_pairs(uint32_t x, uint32_t (&p)[4]) {
-  const uint32_t y = x >> 8;
-  p[0] = x & 0x000f000fu;
-  p[1] = x & 0x00f000f0u;
-  p[2] = y & 0x000f000fu;
-  p[3] = y & 0x00f000f0u;
+  const uint32_t y = x << 2, z = x >> 6;
+  p[0] = y & 0x003c003cu;
+  p[1] = y & 0x03c003c0u;
+  p[2] = z & 0x003c003cu;
+  p[3] = z & 0x03c003c0u;
 }
 // All four as codes (or 15 less the codes) times 2^-20.
 template <bool COMPLEMENT>
@@ -431,7 +433,7 @@ __global__ void __launch_bounds__((Smem<D, NT>::THREADS), 1)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int src = (2 * t + c) * 4;
-        rho[j][c] = __shfl_sync(0xffffffffu, ro, src) * 16777216.f;
+        rho[j][c] = __shfl_sync(0xffffffffu, ro, src) * 4194304.f;
         sigma[j][c] = __shfl_sync(0xffffffffu, so, src);
         lim[j][c] = __shfl_sync(0xffffffffu, lo, src);
       }
