@@ -17,8 +17,8 @@
 //   So K's codes enter as code 2^-22 and code 2^-18 (one shift for two pairs; q is
 //   divided by 16 where it meets the larger ones): with 2^-24 and 2^-20, half a shift
 //   less, lse was up to 1.1e-5 off for fp16 q and short requests, 3e-6 so (193 us and
-//   196 us below; all at 2^-20, a shift more, 202 us).  V takes all codes at 2^-20, which over a million tokens
-//   shows (0.0016 off, below, and 0.0019 with 2^-24).
+//   196 us below; all at 2^-20, a shift more, 202 us).  V takes all codes at 2^-20,
+//   which over a million tokens shows (0.0016 off, below, and 0.0019 with 2^-24).
 // * The 8 is taken off V's codes after the product, so that nothing is done to
 //   a single code: one more matrix instruction per block forms the sum of
 //   the rounded p vs.  Two blocks go through together, and the second enters

@@ -572,6 +572,26 @@ def test_batches_around_the_ways_to_divide_them(ra, R):
     attend(ra, Batch(ra, lens, [1 + r % 3 for r in range(R)], 4, 2, 64, 32, torch.bfloat16, 63 + R))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_lse_of_short_requests(ra, d):
+    """q . code and zero sum(q) cancel in a score.  Neither, nor a partial sum, is
+    above sum|q| (15 step + |zero|) scale; d / 16 instructions and four fp32
+    operations each cut off 2^-23 of that at most.  exp, its sum and log add
+    2^-20."""
+    b = Batch(ra, [1, 2, 3, 5, 2, 1, 4, 7], [1] * 8, 8, 2, d, 16, torch.float16, 64)
+    scale = 1 / math.sqrt(d)
+    _, lse = ra.kv4_fwd(b.q.cuda(), b.cache, b.table, b.len_t, cu=b.cu, scale=scale)
+    ra.check_status()
+    for r in range(8):
+        (kc, ks, kz), (vc, vs, vz) = b.kv[r]
+        _, ref, _ = kv4.kv4_attention(b.q[r:r + 1].double().numpy(), kv4.kv4_values(kc, ks, kz),
+                                      kv4.kv4_values(vc, vs, vz), 1, False, scale)
+        got = lse[r].double().cpu().numpy()
+        q = b.q[r].double().abs().sum(-1).numpy()
+        most = q * scale * (15 * float(np.max(ks)) + float(np.max(np.abs(kz))))
+        assert (np.abs(got - ref[0]) <= most * (d / 16 + 4) * 2.0 ** -23 + 2.0 ** -20).all()
+
+
 def test_a_table_far_wider_than_the_lengths(ra):
     """2^20 columns of 1024 tokens: the line of work is then counted in groups
     of blocks, so that its longest possible form fits 32 bits."""
