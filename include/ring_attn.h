@@ -398,6 +398,8 @@ enum { RA_BF16 = 0, RA_FP16 = 1, RA_FP32 = 2 };
  *                                       tokens, a stack beyond num_pages)   (out)
  * With a shortage nothing changes: the outputs are the inputs, cu is 0 and
  * every slot -1.  Entries of the table beyond a request's pages are not read.
+ * A page index outside [0, num_pages) in the table or the stack moves between
+ * them as any other, its tokens' slots are -1, and it is reported.
  *
  * Each of lens_out, table_out, pool_out is either the input itself or does not
  * overlap any other argument.  R <= 8192, W >= 1, R * W < 2^31,

@@ -72,7 +72,8 @@ def kv4_unpack(cache: np.ndarray, page: int, d: int):
 
 def kv4_plan(lens, add, table, pool, page: int, max_tokens: int):
     """One step of the page plan on Python lists (table: a list of lists):
-    (lens, table, pool, cu, slots, shortage)."""
+    (lens, table, pool, cu, slots, shortage).  A page index outside the cache
+    gives no slots."""
     R, W, num_pages = len(lens), len(table[0]) if table else 0, len(pool) - 1
     same = (list(lens), [list(r) for r in table], list(pool), [0] * (R + 1), [-1] * max_tokens)
     pages = lambda n: -(-n // page)  # noqa: E731
@@ -100,7 +101,8 @@ def kv4_plan(lens, add, table, pool, page: int, max_tokens: int):
             for j in range(pages(lens[r]), pages(lens[r] + add[r])):
                 table2[r][j] = stack.pop()
             for p in range(lens[r], lens[r] + add[r]):
-                slots.append(table2[r][p // page] * page + p % page)
+                at = table2[r][p // page]
+                slots.append(at * page + p % page if 0 <= at < num_pages else -1)
             lens2[r] += add[r]
         cu.append(len(slots))
     pool2 = [len(stack)] + stack + [-1] * (num_pages - len(stack))

@@ -410,9 +410,10 @@ def kv4_plan(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, pool: t
     Returns (lens, table, pool, cu [R + 1], slots [max_tokens], shortage [1]):
     the state after the step, the new tokens before each request, their slots
     (-1 behind the last) and 0, or how many pages are missing (-1: numbers
-    that do not fit), in which case nothing changes.  ``out``: tensors of
-    these shapes for the results; the first three may be the inputs
-    themselves."""
+    that do not fit), in which case nothing changes.  A page index outside
+    [0, num_pages) gives slots of -1 and is reported by ``check_status``.
+    ``out``: tensors of these shapes for the results; the first three may be
+    the inputs themselves."""
     if not (isinstance(table, torch.Tensor) and table.is_cuda and table.dtype is _i32
             and table.dim() == 2 and table.is_contiguous()):
         _check_cuda(table, "table", _i32, 2)

@@ -28,7 +28,10 @@ __device__ unsigned long long g_kv4_cache_status = 0ull;
 // outputs may be the inputs), released pages are on the stack before they
 // are taken again, the table is complete before the slots read it.  The
 // stack positions follow from the prefix sums alone, so the result does not
-// depend on which thread does what.
+// depend on which thread does what.  A page index outside the cache (of a table or
+// a stack that something else spoiled) keeps its place in them, is reported, and
+// gives no slots: page * p.page of such an index may be any slot of another
+// request, or pass for the -1 of no slot.
 //
 // Bound by latency: 6.4 us for 8 requests (one CTA), 15.6 us for 1000 requests
 // with a table of 1000 x 256 that is copied and 18.5K slots (eight CTAs), of which
@@ -171,9 +174,12 @@ __global__ void __launch_bounds__(PLAN_THREADS) ra_kv4_plan_kernel(const Kv4Plan
     // above the stack's new top nothing is left
     for (int i = itop + 1 + gtid; i <= p.num_pages; i += gsize) p.pool_out[i] = -1;
   }
+  bool outside = false;   // a page index outside the cache
   for (int i = gtid; i < n_rel; i += gsize) {
     const int r = find_request(s_rel, R + 1, i);
-    p.pool_out[n_free + 1 + i] = p.table[static_cast<long long>(r) * p.W + (i - s_rel[r])];
+    const int page = p.table[static_cast<long long>(r) * p.W + (i - s_rel[r])];
+    outside |= page < 0 || page >= p.num_pages;
+    p.pool_out[n_free + 1 + i] = page;
   }
   for (int r = gtid; r < R; r += gsize) {
     p.cu[r] = keep ? 0 : s_cu[r];
@@ -197,6 +203,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) ra_kv4_plan_kernel(const Kv4Plan
     const int at = itop - i;        // from the top of the stack
     const int page = at <= n_free ? __ldcg(p.pool + at) : __ldcg(p.pool_out + at);
     const int old = (s_len[r] + p.page - 1) / p.page;
+    outside |= page < 0 || page >= p.num_pages;
     p.table_out[static_cast<long long>(r) * p.W + old + (i - s_take[r])] = page;
     p.pool_out[at] = -1;
   }
@@ -208,11 +215,15 @@ __global__ void __launch_bounds__(PLAN_THREADS) ra_kv4_plan_kernel(const Kv4Plan
     if (i < n_tok) {
       const int r = find_request(s_cu, R + 1, static_cast<int>(i));
       const int pos = s_len[r] + (static_cast<int>(i) - s_cu[r]);
-      slot = __ldcg(p.table_out + static_cast<long long>(r) * p.W + pos / p.page) * p.page +
-             pos % p.page;
+      const int page = __ldcg(p.table_out + static_cast<long long>(r) * p.W + pos / p.page);
+      if (page < 0 || page >= p.num_pages)
+        outside = true;
+      else
+        slot = page * p.page + pos % p.page;
     }
     p.slots[i] = slot;
   }
+  if (outside) kv4_record(&g_kv4_cache_status, RA_ERR_INVALID_ARG, KV4_SITE_PAGE);
 }
 
 // ------------------------------------------------------------------ append

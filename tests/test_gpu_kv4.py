@@ -127,6 +127,28 @@ def test_plan_of_no_request(ra):
     assert got[4].tolist() == [-1] * 4 and got[5].item() == 0
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_plan_reports_pages_outside_the_cache(ra, in_place):
+    """Indices whose product with the page size is -16 + 15 = -1 (no slot), or
+    wraps to a slot of page 0, or lies just behind the cache: no slots, one
+    report, and the other requests' slots as ever.  One in a table that goes on
+    (its request's last page has room), one released, one taken."""
+    from ring_attention_ordered_b200 import _lib
+    own = [7, 6]
+    for bad in (-1, 1 << 28, (1 << 28) + 1, 8, -(1 << 28)):
+        for lens, add, table, pool in (
+                ([15, 17], [1, 2], [[bad, -1], own], [0] + [-1] * 8),
+                ([20, 17], [-1, 15], [[5, bad], own], [1, 4] + [-1] * 7),
+                ([0, 17], [20, 1], [[-1, -1], own], [2, bad, 3] + [-1] * 6)):
+            check_plan(ra, lens, add, table, pool, 16, 24, in_place)
+            with pytest.raises(_lib.RingAttnError) as e:
+                ra.check_status()
+            assert e.value.status == _lib.RA_ERR_INVALID_ARG
+    # a table's entries behind a request's pages are not read
+    check_plan(ra, [16, 17], [0, 1], [[5, 99], own], [0] + [-1] * 8, 16, 4, in_place)
+    ra.check_status()
+
+
 # ------------------------------------------------------------------ append, read
 def vectors(T, Hkv, d, dtype, seed):
     """k and v with the vectors on which a quantiser can go wrong."""

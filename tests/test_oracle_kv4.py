@@ -112,6 +112,12 @@ def test_plan_keeps_every_page_once():
         assert len(set(live)) == len(live) == new[3][-1]
 
 
+def test_plan_gives_no_slots_of_pages_outside_the_cache():
+    got = kv4.kv4_plan([3, 3], [2, 1], [[-1, -1], [3, -1]], [1, 5, -1, -1, -1], 4, 4)
+    assert got[0] == [5, 4] and got[1] == [[-1, 5], [3, -1]]
+    assert got[4] == [-1, -1, 15, -1] and got[5] == 0
+
+
 def test_attention_is_the_dense_oracle():
     rng = np.random.default_rng(2)
     L, Hq, Hkv, d = 37, 4, 2, 64
