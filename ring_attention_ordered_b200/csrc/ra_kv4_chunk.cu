@@ -1116,6 +1116,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem = *tmem_holder;
   const Ctl cx{abort_flag, p.wait_limit_ns, &g_status};
 
+  // A call of its own, so before the roles take their registers: here every
+  // thread has the launch's, which cover it; behind, warps hold as few as
+  // CONTROL_REGS.
+  if (s_odd && p.rows_min == 0) kv4_fill_empty<D, THREADS>(p, &g_status);
+
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
     softmax_role<D>(p, br, base, tmem, warp >> 2, pieces, held, s_cut, s_last, cx);
@@ -1137,7 +1142,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (s_odd && p.rows_min == 0) kv4_fill_empty<D, THREADS>(p, &g_status);
 }
 
 template <int D>

@@ -585,6 +585,53 @@ def test_row_starts_that_fall_are_refused(ra, R, n):
     attend(ra, b)
 
 
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_single_request_of_many_rows_without_tokens(ra, d, out_dtype):
+    """One request of 70 x 2 rows: the chunk kernel alone serves it, and writes its
+    empty rows and reports its numbers itself.  Rows of no request are left."""
+    from ring_attention_ordered_b200 import _lib
+    n, T = 70, 75
+    b = Batch(ra, [160], [n], 4, 2, d, 16, torch.bfloat16, 70)
+    q = torch.cat([b.q, torch.full((T - n, 4, d), math.nan, dtype=torch.bfloat16)]).cuda()
+    table = b.table[:, :10].contiguous()   # room for 160 tokens
+    ws = ra.kv4_workspace()
+
+    def call(length, starts, causal=True, reported=False):
+        out = torch.full((T, 4, d), 7.0, dtype=out_dtype, device="cuda")
+        lse = torch.full((T, 4), 7.0, device="cuda")
+        ra.kv4_fwd(q, b.cache, table, i32([length]), cu=i32(starts), causal=causal, out=out,
+                   lse=lse, workspace=ws)
+        if reported:
+            with pytest.raises(_lib.RingAttnError) as e:
+                ra.check_status()
+            assert e.value.status == _lib.RA_ERR_INVALID_ARG
+        else:
+            ra.check_status()
+        assert not bool(ws[:_lib.KV4_COUNTER_BYTES].any())
+        return out, lse
+
+    def empty(got, first, last):
+        out, lse = got
+        assert bool((out[first:last] == 0).all()) and bool(torch.isneginf(lse[first:last]).all())
+        for x in got:
+            assert bool((x[:first] == 7).all()) and bool((x[last:] == 7).all())
+
+    empty(call(0, [0, n]), 0, n)
+    empty(call(0, [0, n], causal=False), 0, n)
+    empty(call(0, [2, n]), 2, n)
+    empty(call(-3, [0, n], reported=True), 0, n)
+    empty(call(0, [3, 200], reported=True), 3, T)
+    empty(call(0, [-4, n], reported=True), 0, n)
+    empty(call(160, [n, 3], reported=True), 0, 0)     # the starts fall: nothing is done
+    empty(call(0, [n, 3], reported=True), 0, 0)
+    want = call(160, [0, n])
+    b.check(want[0][:n], want[1][:n], True, 1 / math.sqrt(d), out_dtype)
+    cut = call(10 ** 9, [0, n], reported=True)        # cut down to the table's room
+    assert torch.equal(cut[0], want[0]) and torch.equal(cut[1], want[1])
+    assert bool((want[0][n:] == 7).all()) and bool((want[1][n:] == 7).all())
+
+
 @pytest.mark.parametrize("R", [31, 32, 33, 63, 64, 65])
 def test_batches_around_the_ways_to_divide_them(ra, R):
     """Empty requests, short ones and a long one, in and out of step with the
