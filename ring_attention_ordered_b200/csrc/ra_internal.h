@@ -222,8 +222,13 @@ cudaError_t read_and_clear_kv4_chunk_status(unsigned long long* out);
 // Workspace of kv4 attention: the counters of the decoding kernel, those of
 // the chunk kernel (three a CTA each), then partial results of the pieces into
 // which a launch cuts the work (two a CTA; the two kernels, one after the
-// other on the stream, use the same room).
-constexpr int KV4_MAX_CTAS = 1024, KV4C_MAX_CTAS = 160;
+// other on the stream, use the same room).  A unit's pieces are folded at two
+// levels of KV4_FOLD at most, in room for KV4_FOLD pieces, so a launch has no
+// more CTAs than KV4_FOLD squared.
+constexpr int KV4_FOLD = 16;
+constexpr int KV4_MAX_CTAS = 256, KV4C_MAX_CTAS = 160;
+static_assert(KV4_MAX_CTAS <= KV4_FOLD * KV4_FOLD && KV4C_MAX_CTAS <= KV4_FOLD * KV4_FOLD,
+              "two levels of folds");
 constexpr int KV4_PIECE_FLOATS = 16 * (128 + 2), KV4C_PIECE_FLOATS = 256 * (128 + 2);
 constexpr size_t KV4_COUNTER_BYTES = 3 * KV4_MAX_CTAS * 4;
 constexpr size_t KV4C_COUNTER_BYTES = 3 * KV4C_MAX_CTAS * 4;

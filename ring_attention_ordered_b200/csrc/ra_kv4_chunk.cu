@@ -71,7 +71,7 @@ constexpr int NRAW = 3;       // raw stages (the K or V part of 8 blocks)
 constexpr int NPAR = 4;       // slots of a tile's steps and zeros
 constexpr int UNIT_COST = 2;  // what a unit costs beside its tiles, in tiles
 constexpr int MIN_TILES = 8;  // tiles below which a stretch is not cut further
-constexpr int FOLD = 16;      // pieces that one CTA folds at a time
+constexpr int FOLD = KV4_FOLD;   // pieces that one CTA folds at a time
 constexpr float P_SHIFT = 5.f;         // p = 2^P_SHIFT at the reference
 constexpr float P_LIMIT = 32768.f;     // beyond which the reference moves
 constexpr float Q_SCALE = 256.f;       // of q in fp16, see Rows
@@ -117,6 +117,7 @@ struct Cfg {
   static constexpr int SMEM_BYTES = OFF_UNITS + UQ * 4 + 1024;   // + alignment slack
   static_assert(SMEM_BYTES <= 232448 - 1024, "shared memory budget");
   static_assert(UNIT_ROWS * (D + 2) <= KV4C_PIECE_FLOATS, "workspace piece");
+  static_assert(FOLD * UNIT_ROWS * 4 <= 2 * Q_BYTES, "the factors of a fold fit q's place");
 };
 
 template <int D>

@@ -86,7 +86,7 @@ constexpr int MIN_CELLS = 4;
 // tokens: 36.8 us with 4, 30.9 us with 8, 31.4 us with 12; 8 of 32K tokens and 32
 // heads: 193 us with 4, 191 us with 8, 195 us with 16).
 constexpr int UNIT_COST = 8;
-constexpr int FOLD = 16;           // pieces that one CTA folds at a time
+constexpr int FOLD = KV4_FOLD;     // pieces that one CTA folds at a time
 constexpr float P_SHIFT = 8.f;     // p vs = 2^P_SHIFT at the reference
 constexpr float P_LIMIT = 32768.f;
 
