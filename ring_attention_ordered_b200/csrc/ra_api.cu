@@ -704,7 +704,8 @@ ra_status ring_attn_kv4_plan(const int32_t* lens, const int32_t* add, const int3
   if (R < 0 || num_pages < 0 || max_tokens < 0)
     return fail(RA_ERR_INVALID_ARG, "negative size (R=%d num_pages=%d max_tokens=%lld)", R,
                 num_pages, static_cast<long long>(max_tokens));
-  if (R > 8192) return fail(RA_ERR_UNSUPPORTED, "R=%d (supported: up to 8192 requests)", R);
+  if (R > ra::KV4_PLAN_MAX_R)
+    return fail(RA_ERR_UNSUPPORTED, "R=%d (supported: up to %d requests)", R, ra::KV4_PLAN_MAX_R);
   if (W < 1 || static_cast<long long>(R) * W >= (1ll << 31))
     return fail(RA_ERR_INVALID_ARG, "W must be >= 1 and R * W < 2^31 (R=%d W=%d)", R, W);
   if (page < 1 || page > 4096)

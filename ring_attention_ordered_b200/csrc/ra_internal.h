@@ -153,6 +153,7 @@ cudaError_t launch_quantize_fp8(const __nv_bfloat16* x, uint8_t* codes, float* s
                                 long long L, int H, int d, cudaStream_t stream);
 
 // ---- the paged 4-bit K/V cache (layout and format: ra_kv4.cuh)
+constexpr int KV4_PLAN_MAX_R = 8192;   // requests of a plan: its sums lie in shared memory
 struct Kv4PlanParams {
   const int32_t* lens;    // [R] tokens held by each request
   const int32_t* add;     // [R] tokens to add, -1: the request is done

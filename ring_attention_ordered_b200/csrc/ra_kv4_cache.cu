@@ -38,6 +38,8 @@ __device__ unsigned long long g_kv4_cache_status = 0ull;
 // the bytes are 0.4 us.
 constexpr int PLAN_THREADS = 1024;
 
+constexpr size_t plan_smem_bytes(int R) { return (4 * static_cast<size_t>(R) + 3) * sizeof(int); }
+
 struct PlanSums {
   long long tok;   // new tokens
   int rel;         // released pages
@@ -94,7 +96,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) ra_kv4_plan_kernel(const Kv4Plan
   int* s_cu = plan_smem;             // [R + 1] new tokens before request r
   int* s_rel = s_cu + R + 1;         // [R + 1] released pages before request r
   int* s_take = s_rel + R + 1;       // [R + 1] new pages before request r
-  int* s_len = s_take + R + 1;       // [R]     tokens held before the call
+  int* s_len = s_take + R + 1;       // [R]     tokens held before the call (plan_smem_bytes)
   __shared__ PlanSums s_warp[PLAN_THREADS / 32];
   __shared__ PlanSums s_carry;
   __shared__ int s_bad;
@@ -561,12 +563,21 @@ cudaError_t launch_copy(void (*kernel)(const Kv4CopyParams), const Kv4CopyParams
 }  // namespace
 
 cudaError_t launch_kv4_plan(const Kv4PlanParams& p, cudaStream_t stream) {
-  const size_t smem = static_cast<size_t>(4 * p.R + 3) * sizeof(int);
-  cudaError_t e = cudaSuccess;
-  if (smem > 40 * 1024) {
+  const size_t smem = plan_smem_bytes(p.R);
+  // The limit is the kernel's, not the launch's: set once a device, to what the
+  // largest call needs.  Set to each call's own size, one thread's call lowered it
+  // between another's and its launch, which then failed (25 of 8000 launches of two
+  // threads with 8192 and 2600 requests).
+  static int configured_dev[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured_dev[dev]) {
     e = cudaFuncSetAttribute(ra_kv4_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem));
+                             static_cast<int>(plan_smem_bytes(KV4_PLAN_MAX_R)));
     if (e != cudaSuccess) return e;
+    configured_dev[dev] = 1;
   }
   // One CTA for what one CTA's threads do in a few rounds, else a cluster.
   long long work = p.max_tokens;

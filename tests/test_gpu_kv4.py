@@ -127,6 +127,42 @@ def test_plan_of_no_request(ra):
     assert got[4].tolist() == [-1] * 4 and got[5].item() == 0
 
 
+def test_plans_of_several_threads(ra):
+    """Large and smaller plans launched by threads at the same time, through the C
+    entry, which does not hold the interpreter: none takes another's room for its
+    sums."""
+    import threading
+
+    from ring_attention_ordered_b200 import _lib
+    plan = _lib.function("ring_attn_kv4_plan")
+    kept, bad = [], []
+
+    def arguments(R):
+        lens, add, pool = i32([0] * R), i32([0] * R), ra.kv4_pool(1)
+        table = torch.full((R, 1), -1, dtype=torch.int32, device="cuda")
+        t = [lens, add, table, pool, lens, table, pool, i32([9] * (R + 1)), i32([0]), i32([9])]
+        s = torch.cuda.Stream()
+        kept.append((t, s))
+        return [x.data_ptr() for x in t] + [R, 1, 1, 16, 0, s.cuda_stream]
+
+    def run(args, go):
+        go.wait()
+        bad.extend(st for st in (plan(*args) for _ in range(6000)) if st)
+
+    calls = [arguments(R) for R in (8192, 2600, 8191)]
+    torch.cuda.synchronize()
+    go = threading.Barrier(len(calls))
+    threads = [threading.Thread(target=run, args=(a, go)) for a in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not bad, (len(bad), bad[0])
+    for t, _ in kept:
+        assert t[9].item() == 0 and not bool(t[7].any()) and t[3].tolist() == [1, 0]
+
+
 @pytest.mark.parametrize("in_place", [False, True])
 def test_plan_reports_pages_outside_the_cache(ra, in_place):
     """Indices whose product with the page size is -16 + 15 = -1 (no slot), or
