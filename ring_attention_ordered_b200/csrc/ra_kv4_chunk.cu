@@ -7,16 +7,21 @@
 //   over the tokens they see.  One CTA per SM; the roles and the order of the
 //   MMAs are the bf16 forward's (ra_fwd_roles.cuh).
 // * Warps 0-3 and 4-7 own a row tile each: they bring their rows' q into
-//   shared memory (fp16, scaled by a power of two, exact), read S from tensor
+//   shared memory (fp16, scaled by a power of two: see Rows), read S from tensor
 //   memory, form s = ks C + kz sum(q) in fp32 (C = q . codes; the steps
 //   and zeros lie in shared memory), keep the reference and the running sum, and
 //   write P in fp16 over S.
 // * Warp 8 copies the blocks' K and V parts into a ring of raw stages; warps
 //   12-15 turn them into fp16 operand tiles (128-byte swizzle): the codes of K
-//   as they are, as subnormal fp16 numbers (one AND a pair), so S has no
-//   rounding beyond fp32; the values of V, step * code + zero rounded to fp16
+//   as subnormal fp16 numbers, code 2^-22 and code 2^-18 (one AND a pair and a shift
+//   for two), the values of V, step * code + zero rounded to fp16
 //   (half a step, 2^-11 of the value at most, next to an output of that
 //   precision at most).  One unpacking serves 256 rows.
+//   The products of subnormal numbers lose places where an instruction aligns them,
+//   which shows in lse of rows that see few tokens, the first of a prompt: relative
+//   error for fp16 q 1.1e-6 with the nibbles where they lie (2^-24 and 2^-20, half a
+//   shift less, 552 us below), 2.2e-7 so (560 us), 1.8e-7 as normal numbers by a fused
+//   multiply-add a pair (577 us); 1.1e-7 in plain 32-bit arithmetic.
 // * P = 2^(s - m + 5) in fp16.  m is a maximum of the row that is moved, and O
 //   rescaled, only when P would pass 2^15: so a tile takes one pass over S, no
 //   separate search for its maximum, and what lies up to 2^29 below the
@@ -444,7 +449,8 @@ __device__ void unpack_role(const Kv4AttnParams& p, const Bars& br, uint32_t bas
         if (v == 0) {
           // K: 16 bytes are 32 codes of one token, four swizzle chunks; the
           // eight lanes of a phase take eight tokens, whose chunks then lie in
-          // eight places
+          // eight places.  Nibbles (0, 4), (1, 5), (2, 6), (3, 7) of a word are pairs
+          // of code 2^-22, 2^-18, 2^-22, 2^-18
           constexpr int CPR = D / 32;                    // 16-byte parts of a row
 #pragma unroll 1
           for (int q = 0; q < CPR; ++q) {
@@ -453,9 +459,9 @@ __device__ void unpack_role(const Kv4AttnParams& p, const Bars& br, uint32_t bas
             const uint32_t row = dst + (q >> 1) * BOX_BYTES + i * 128;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              const uint32_t y = x[w] >> 8;
-              sts128(row + (((q & 1) * 4 + w) ^ (i & 7)) * 16, x[w] & 0x000f000fu,
-                     x[w] & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u);
+              const uint32_t y = x[w] << 2, z = x[w] >> 6;
+              sts128(row + (((q & 1) * 4 + w) ^ (i & 7)) * 16, y & 0x003c003cu,
+                     y & 0x03c003c0u, z & 0x003c003cu, z & 0x03c003c0u);
             }
           }
           // step and zero of token i: pairs of tokens as (step, step, zero, zero)
@@ -465,7 +471,7 @@ __device__ void unpack_role(const Kv4AttnParams& p, const Bars& br, uint32_t bas
           const uint32_t par =
               base + C::OFF_PAR + (tile % NPAR) * TILE_KEYS * 8 + (i >> 1) * 16 + (i & 1) * 4;
           asm volatile("st.shared.f32 [%0], %1;" ::"r"(par),
-                       "f"(sz.x * (p.scale_log2 * (16777216.f / Q_SCALE))) : "memory");
+                       "f"(sz.x * (p.scale_log2 * (4194304.f / Q_SCALE))) : "memory");
           asm volatile("st.shared.f32 [%0], %1;" ::"r"(par + 8), "f"(sz.y * p.scale_log2) : "memory");
           if (i == 0) held[NRAW + tile % NPAR] = have;
           mbar_arrive(br.par_full(tile % NPAR));
@@ -550,10 +556,13 @@ __device__ void unpack_role(const Kv4AttnParams& p, const Bars& br, uint32_t bas
 // sums are joined over the four lanes of a row once, at the end of a piece.
 //
 // Scores in log2 units are s = C ks' + kz' sigma with ks' = ks scale log2(e)
-// 2^(24 - Q_SHIFT) and kz' = kz scale log2(e), which the unpacking warps
-// prepare; q is scaled by 2^Q_SHIFT for every row, so the exponent s - m + 5 is
-// two fused multiply-adds.  A row whose magnitudes that scale would take out
-// of fp16's range has a scale of its own, and its C a factor `f`.
+// 2^22 / Q_SCALE and kz' = kz scale log2(e), which the unpacking warps
+// prepare; q is scaled by Q_SCALE for every row (and divided by 16 where it meets
+// the larger codes), so the exponent s - m + 5 is two fused multiply-adds.  A row
+// whose magnitudes that scale would take out of fp16's range has a scale of its own,
+// and its C a factor `f`.  Scaled so, q is exact in fp16 but for elements that are
+// small in a row of small ones: with the largest at 2^-14, the least the common scale
+// is used for, they are off by 2^-15 of it, and scores by 2^-29 |k|.
 struct Rows {
   uint64_t sigma2[4];   // sum of q, twice
   float f[4];
