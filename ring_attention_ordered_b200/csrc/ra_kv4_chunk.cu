@@ -74,6 +74,11 @@ static_assert(256 * SOFTMAX_REGS + 128 * CONTROL_REGS + 128 * UNPACK_REGS <= THR
 constexpr int NS = 4;         // operand stages (K or V tile)
 constexpr int NRAW = 3;       // raw stages (the K or V part of 8 blocks)
 constexpr int NPAR = 4;       // slots of a tile's steps and zeros
+// Pieces that the loader has under way, the one in hand among them (prompts as one
+// call, 32 query and 8 K/V heads, d = 128: 64 of 200 tokens 289 us with 1, 274 with 2,
+// 286 with 3, 298 with 4; 128 of 60 tokens 146, 134, 134, 134 us; longer ones alike).
+constexpr int AHEAD = 2;
+static_assert(AHEAD < UQ, "a place of the queue is free when the piece AHEAD before is done");
 constexpr int UNIT_COST = 2;  // what a unit costs beside its tiles, in tiles
 constexpr int MIN_TILES = 8;  // tiles below which a stretch is not cut further
 constexpr int FOLD = KV4_FOLD;   // pieces that one CTA folds at a time
@@ -116,7 +121,7 @@ struct Cfg {
   static constexpr int OFF_RAW = OFF_KV + NS * KV_BYTES;
   static constexpr int OFF_PAR = OFF_RAW + NRAW * RAW_BYTES;
   static constexpr int OFF_BAR = OFF_PAR + NPAR * TILE_KEYS * 8;
-  static constexpr int NUM_BARS = fwd_num_bars(NS) + 2 * NRAW + NPAR + 2;
+  static constexpr int NUM_BARS = fwd_num_bars(NS) + 2 * NRAW + NPAR + UQ + 1;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_UNITS = OFF_MISC + 16;
   static constexpr int SMEM_BYTES = OFF_UNITS + UQ * 4 + 1024;   // + alignment slack
@@ -156,17 +161,22 @@ struct Geom {
 };
 
 struct Bars : FwdBars {
-  uint32_t raw_full0, raw_empty0, par_full0, unit_done, rows;
+  uint32_t raw_full0, raw_empty0, par_full0, unit_done0, rows;
   __device__ __forceinline__ uint32_t raw_full(int s) const { return raw_full0 + 8u * s; }
   __device__ __forceinline__ uint32_t raw_empty(int s) const { return raw_empty0 + 8u * s; }
   __device__ __forceinline__ uint32_t par_full(int s) const { return par_full0 + 8u * s; }
+  // Piece k is done: one barrier a place of the queue, so that the phase waited for is
+  // the place's latest or the one before.  With one for all, a wait for a piece two
+  // back blocked until the one in hand was done, and the softmax group that skips a
+  // second row tile without rows arrived in the other's phase.
+  __device__ __forceinline__ uint32_t unit_done(int k) const { return unit_done0 + 8u * (k % UQ); }
   __device__ __forceinline__ void place(uint32_t bar0, uint32_t units_addr) {
     layout(bar0, NS, units_addr);
     raw_full0 = bar0 + 8u * fwd_num_bars(NS);
     raw_empty0 = raw_full0 + 8u * NRAW;
     par_full0 = raw_empty0 + 8u * NRAW;
-    unit_done = par_full0 + 8u * NPAR;
-    rows = unit_done + 8u;
+    unit_done0 = par_full0 + 8u * NPAR;
+    rows = unit_done0 + 8u * UQ;
   }
   __device__ __forceinline__ void start() const {
     mbar_init(q_full, 256);
@@ -189,7 +199,7 @@ struct Bars : FwdBars {
       mbar_init(raw_empty(s), 128);
     }
     for (int s = 0; s < NPAR; ++s) mbar_init(par_full(s), 128);
-    mbar_init(unit_done, 256);
+    for (int i = 0; i < UQ; ++i) mbar_init(unit_done0 + 8u * i, 256);
     mbar_init(rows, 256);
   }
 };
@@ -297,6 +307,10 @@ __device__ void loader_role(const Kv4AttnParams& p, const Bars& br, uint32_t bas
   uint32_t it = 0;         // raw stages filled
   uint32_t tiles_done = 0; // tiles of tokens handed out
   int k = 0;
+  auto place_for = [&](int k) {
+    return k < AHEAD ||
+           wait_warp(br.unit_done(k - AHEAD), ((k - AHEAD) / UQ) & 1u, cx, SITE_DONE);
+  };
   long long at = st.per * blockIdx.x;
   const long long end = min(at + st.per, st.total);
   int r = 0;
@@ -332,8 +346,7 @@ __device__ void loader_role(const Kv4AttnParams& p, const Bars& br, uint32_t bas
       const int row0 = rt * UNIT_ROWS;
       const int t0 = max(off - first, 0), t1 = min(off + cells - first, nt);
       if (t1 <= t0) continue;
-      if (k >= UQ - 1 &&
-          !wait_warp(br.unit_done, (k - (UQ - 1)) & 1u, cx, SITE_DONE)) goto drain;
+      if (!place_for(k)) goto drain;
       if (lane == 0) {
         Piece x;
         x.n_kv = t1 - t0;
@@ -386,7 +399,7 @@ __device__ void loader_role(const Kv4AttnParams& p, const Bars& br, uint32_t bas
       }
     }
   }
-  if (k >= UQ - 1 && !wait_warp(br.unit_done, (k - (UQ - 1)) & 1u, cx, SITE_DONE)) goto drain;
+  if (!place_for(k)) goto drain;
   if (lane == 0) {
     asm volatile("st.shared.s32 [%0], %1;" ::"r"(br.units + 4u * (k % UQ)), "r"(-1) : "memory");
     mbar_arrive(br.unit_full(k));
@@ -1056,7 +1069,7 @@ __device__ void softmax_role(const Kv4AttnParams& p, const Bars& br, uint32_t ba
       }
       ++n_cut;
     }
-    mbar_arrive(br.unit_done);
+    mbar_arrive(br.unit_done(k));
   }
 
   // ---- units that cross CTAs, one from before this CTA and one to behind it: the

@@ -568,6 +568,27 @@ def test_any_split_gives_the_result(ra, n):
         _lib.ring_attn_set_max_ctas(0)
 
 
+@pytest.mark.parametrize("d,dtype", [(64, torch.float16), (128, torch.bfloat16)])
+@pytest.mark.parametrize("ctas", [1, 2, 5])
+def test_many_short_units_a_cta(ra, ctas, d, dtype):
+    """Prompts and chunks whose units, with and without a second row tile, far outnumber
+    the places of a CTA's queue; among them single tokens and an empty request."""
+    from ring_attention_ordered_b200 import _lib
+    n = [70, 33, 1, 129, 40, 257, 64, 0, 65, 35, 100, 160]
+    lens = [a + b for a, b in zip(n, [0, 0, 50, 0, 300, 0, 129, 0, 1, 700, 0, 30])]
+    b = Batch(ra, lens, n, 8, 2, d, 16, dtype, 71)
+    ws = ra.kv4_workspace()
+    try:
+        _lib.ring_attn_set_max_ctas(ctas)
+        first = attend(ra, b, workspace=ws)
+        for _ in range(3):
+            again = attend(ra, b, workspace=ws)
+            assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+        assert not bool(ws[:_lib.KV4_COUNTER_BYTES].any())
+    finally:
+        _lib.ring_attn_set_max_ctas(0)
+
+
 def test_one_long_request(ra):
     """100001 tokens: a stretch of the request on every CTA."""
     b = Batch(ra, [100001], [1], 2, 1, 128, 128, torch.bfloat16, 22)
