@@ -351,7 +351,8 @@ enum { RA_BF16 = 0, RA_FP16 = 1, RA_FP32 = 2 };
  *
  *   cache   uint8 [num_pages, Hkv, page / 16, 16 (d + 8)], contiguous,
  *           16-byte aligned; page (tokens a page) a multiple of 16 up to
- *           4096, d 64 or 128, num_pages * page < 2^31.  The last axis is one
+ *           4096, d 64 or 128, num_pages * page < 2^31; NULL is allowed for
+ *           one of no pages.  The last axis is one
  *           block, 16 tokens of one page and head: K codes (16 rows of d / 2
  *           bytes, element 2i in the low nibble of byte i), 16 (step, zero)
  *           fp16 pairs of K, V codes, 16 pairs of V.  The V codes of the

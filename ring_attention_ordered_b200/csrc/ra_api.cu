@@ -752,10 +752,10 @@ ra_status ring_attn_kv4_append(const void* k, int64_t k_stride, const void* v, i
   if (k_stride < width || v_stride < width || k_stride % 8 != 0 || v_stride % 8 != 0)
     return fail(RA_ERR_INVALID_ARG, "token strides must be multiples of 8 and >= Hkv * d");
   if (T == 0) return ok();
-  if (!k || !v || !slots || !cache) return fail(RA_ERR_INVALID_ARG, "null pointer");
+  const size_t nc = kv4_cache_bytes(Hkv, d, num_pages, page);
+  if (!k || !v || !slots || (!cache && nc != 0)) return fail(RA_ERR_INVALID_ARG, "null pointer");
   if (!aligned16(k) || !aligned16(v) || !aligned16(cache) || !aligned4(slots))
     return fail(RA_ERR_INVALID_ARG, "k, v and cache must be 16-byte aligned, slots 4-byte aligned");
-  const size_t nc = kv4_cache_bytes(Hkv, d, num_pages, page);
   if (nc != 0 && (overlaps(cache, nc, k, span_bytes(T, width, k_stride, 2)) ||
                   overlaps(cache, nc, v, span_bytes(T, width, v_stride, 2)) ||
                   overlaps(cache, nc, slots, static_cast<size_t>(T) * 4)))
@@ -787,10 +787,10 @@ ra_status ring_attn_kv4_read(const void* cache, const int32_t* slots, void* k, v
   if (dtype != RA_BF16 && dtype != RA_FP16 && dtype != RA_FP32)
     return fail(RA_ERR_UNSUPPORTED, "dtype %d (supported: RA_BF16, RA_FP16, RA_FP32)", dtype);
   if (T == 0) return ok();
-  if (!k || !v || !slots || !cache) return fail(RA_ERR_INVALID_ARG, "null pointer");
+  const size_t nc = kv4_cache_bytes(Hkv, d, num_pages, page);
+  if (!k || !v || !slots || (!cache && nc != 0)) return fail(RA_ERR_INVALID_ARG, "null pointer");
   if (!aligned16(k) || !aligned16(v) || !aligned16(cache) || !aligned4(slots))
     return fail(RA_ERR_INVALID_ARG, "k, v and cache must be 16-byte aligned, slots 4-byte aligned");
-  const size_t nc = kv4_cache_bytes(Hkv, d, num_pages, page);
   const size_t no = static_cast<size_t>(T) * Hkv * d * (dtype == RA_FP32 ? 4 : 2);
   const size_t ns = static_cast<size_t>(T) * 4;
   if ((nc != 0 && (overlaps(cache, nc, k, no) || overlaps(cache, nc, v, no))) ||
@@ -862,7 +862,8 @@ ra_status ring_attn_kv4_fwd(const void* q, int64_t q_stride, const void* cache,
     return fail(RA_ERR_UNSUPPORTED,
                 "too many requests and rows (T=%lld R=%d Hq=%d): their tiles of 8 rows times "
                 "the K/V heads must be <= 2^24", static_cast<long long>(T), R, Hq);
-  if (!q || !cache || !table || !lens || !out || !lse || !workspace)
+  const size_t nc = kv4_cache_bytes(Hkv, d, num_pages, page);
+  if (!q || (!cache && nc != 0) || !table || !lens || !out || !lse || !workspace)
     return fail(RA_ERR_INVALID_ARG, "null pointer");
   if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || !aligned16(workspace))
     return fail(RA_ERR_INVALID_ARG, "q, cache, out and workspace must be 16-byte aligned");
@@ -873,8 +874,7 @@ ra_status ring_attn_kv4_fwd(const void* q, int64_t q_stride, const void* cache,
                 workspace_bytes, ra::KV4_WORKSPACE_BYTES);
   const size_t nR = static_cast<size_t>(R) * 4;
   const void* ins[5] = {q, cache, table, lens, cu};
-  const size_t in_n[5] = {span_bytes(T, width, q_stride, 2), kv4_cache_bytes(Hkv, d, num_pages, page),
-                          nR * W, nR, cu ? nR + 4 : 0};
+  const size_t in_n[5] = {span_bytes(T, width, q_stride, 2), nc, nR * W, nR, cu ? nR + 4 : 0};
   const void* outs[3] = {out, lse, workspace};
   const size_t out_n[3] = {static_cast<size_t>(T) * width * (out_dtype == RA_FP32 ? 4 : 2),
                            static_cast<size_t>(T) * Hq * 4, ra::KV4_WORKSPACE_BYTES};

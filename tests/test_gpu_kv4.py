@@ -772,6 +772,28 @@ def test_a_table_far_wider_than_the_lengths(ra):
     attend(ra, b)
 
 
+@pytest.mark.parametrize("n", [1, 70])
+def test_a_cache_of_no_pages(ra, n):
+    """Nothing cached: every row is empty; slots and lengths beyond it are reported."""
+    from ring_attention_ordered_b200 import _lib
+    cache = ra.kv4_cache(0, 2, 64, 16)
+    q = torch.randn(2 * n, 4, 64, device="cuda").to(torch.bfloat16)
+    none, cu = i32([-1] * (2 * n)), i32([0, n, 2 * n])
+    table = i32([[-1, -1]] * 2)
+    ra.kv4_append(q[:, :2], q[:, 2:], none, cache)
+    assert all(bool((x == 0).all()) for x in ra.kv4_read(cache, none))
+    for lens in ([0, 0], [0, 9]):
+        out, lse = ra.kv4_fwd(q, cache, table, i32(lens), cu=cu, causal=False)
+        assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+        if lens[1]:
+            with pytest.raises(_lib.RingAttnError):
+                ra.check_status()
+        ra.check_status()
+    ra.kv4_append(q[:, :2], q[:, 2:], i32([0] + [-1] * (2 * n - 1)), cache)
+    with pytest.raises(_lib.RingAttnError):
+        ra.check_status()
+
+
 def test_many_requests(ra):
     """More requests than threads, most of them short or empty."""
     r = random.Random(5)

@@ -118,6 +118,14 @@ def test_empty_calls_launch_nothing(lib):
     assert fwd(lib, T=0, R=0, cu=0, q=0, out=0, lse=0, ws=0, wsb=0) == _lib.RA_OK
 
 
+def test_a_cache_of_no_pages_needs_no_memory(lib):
+    """Its pointer is NULL (an empty tensor's is): such calls are not refused for
+    it, those to a cache that has pages are."""
+    for call in (append, read, fwd):
+        assert call(lib, cache=0) == INV
+        assert call(lib, cache=0, num_pages=0) != INV, _lib.last_error()
+
+
 def test_workspace_size(lib):
     assert _lib.ring_attn_kv4_workspace_size() > 0
     assert lib.ring_attn_kv4_workspace_size(None) == INV
