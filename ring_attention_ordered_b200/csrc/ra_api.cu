@@ -715,7 +715,8 @@ ra_status ring_attn_kv4_plan(const int32_t* lens, const int32_t* add, const int3
   if (max_tokens >= (1ll << 31)) return fail(RA_ERR_INVALID_ARG, "max_tokens must be < 2^31");
   if (num_pages == 2147483647 || static_cast<long long>(num_pages) * page >= (1ll << 31))
     return fail(RA_ERR_INVALID_ARG, "num_pages * page must be < 2^31");
-  const void* ptrs[10] = {lens, add, table, pool, lens_out, table_out, pool_out, cu, slots, shortage};
+  const void* ptrs[10] = {lens,      add,      table, pool,  lens_out,
+                          table_out, pool_out, cu,    slots, shortage};
   const size_t nR = static_cast<size_t>(R) * 4, nT = nR * W;
   const size_t nP = (static_cast<size_t>(num_pages) + 1) * 4;
   const size_t n[10] = {nR, nR, nT, nP, nR, nT, nP, nR + 4, static_cast<size_t>(max_tokens) * 4, 4};
@@ -918,15 +919,17 @@ ra_status ring_attn_kv4_fwd(const void* q, int64_t q_stride, const void* cache,
   cudaError_t e = cudaSuccess;
   if (decode) {
     prm.counters = reinterpret_cast<unsigned*>(ws);
-    e = ra::launch_kv4_decode(prm, d, static_cast<int>(rows < kKv4DecodeRows ? rows : kKv4DecodeRows),
-                              sms, g_max_ctas.load(), reinterpret_cast<cudaStream_t>(stream));
+    const int most = static_cast<int>(rows < kKv4DecodeRows ? rows : kKv4DecodeRows);
+    e = ra::launch_kv4_decode(prm, d, most, sms, g_max_ctas.load(),
+                              reinterpret_cast<cudaStream_t>(stream));
   }
   if (e == cudaSuccess && chunk) {
     prm.counters = reinterpret_cast<unsigned*>(ws + ra::KV4_COUNTER_BYTES);
     e = ra::launch_kv4_chunk(prm, d, sms, g_max_ctas.load(),
                              reinterpret_cast<cudaStream_t>(stream));
   }
-  if (e != cudaSuccess) return fail(RA_ERR_CUDA, "cache attention launch: %s", cudaGetErrorString(e));
+  if (e != cudaSuccess)
+    return fail(RA_ERR_CUDA, "cache attention launch: %s", cudaGetErrorString(e));
   return ok();
 }
 

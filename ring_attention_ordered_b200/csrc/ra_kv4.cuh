@@ -60,7 +60,7 @@ struct Kv4 {
 
 // Device status word of the kv4 kernels: 0 = ok, else (code << 32) | site << 16 | CTA.
 enum Kv4Site : uint32_t {
-  KV4_SITE_COPY = 1, KV4_SITE_SLOT, KV4_SITE_PAGE, KV4_SITE_LENGTH, KV4_SITE_ROWS, KV4_SITE_TILE
+  KV4_SITE_COPY = 1, KV4_SITE_SLOT, KV4_SITE_PAGE, KV4_SITE_LENGTH
 };
 __device__ __forceinline__ void kv4_record(unsigned long long* status, int code, uint32_t site) {
   atomicCAS(status, 0ull, (static_cast<unsigned long long>(code) << 32) |

@@ -128,7 +128,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) ra_kv4_plan_kernel(const Kv4Plan
           x.rel = old;
         } else {
           x.tok = add;
-          x.take = static_cast<int>((static_cast<long long>(len) + add + p.page - 1) / p.page) - old;
+          x.take =
+              static_cast<int>((static_cast<long long>(len) + add + p.page - 1) / p.page) - old;
         }
       }
       s_len[r] = len;
@@ -169,7 +170,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) ra_kv4_plan_kernel(const Kv4Plan
 
   cluster.sync();   // every CTA has read lens, add and pool[0]
 
-  if (p.table_out != p.table) copy_ints(p.table_out, p.table, static_cast<long long>(R) * p.W, gtid, gsize);
+  if (p.table_out != p.table)
+    copy_ints(p.table_out, p.table, static_cast<long long>(R) * p.W, gtid, gsize);
   if (p.pool_out != p.pool)
     copy_ints(p.pool_out + 1, p.pool + 1, keep ? p.num_pages : min(left, n_free), gtid, gsize);
   if (!keep) {
@@ -268,7 +270,8 @@ __device__ __forceinline__ uint32_t kv4_code(float x, float zero, float step, fl
 }
 
 // Sixteen values of one lane; the LANES lanes of the vector agree on its
-// range.  `use`: whether anything is made of the result.  Returns the codes (element i in nibble i) and the parameter word.
+// range.  `use`: whether anything is made of the result.  Returns the codes (element
+// i in nibble i) and the parameter word.
 //
 // The codes come from t = (x - zero) / step rounded to an integer by adding 1.5
 // * 2^23, four codes joined as one float below 2^24.  The quotient by the
@@ -281,7 +284,7 @@ __device__ __forceinline__ uint32_t kv4_code(float x, float zero, float step, fl
 //
 // The quotient (max - min) / 15 is formed by Markstein's method, a product by
 // the rounded reciprocal and one correction, which gives the correctly rounded
-// one (checked for every significand in nine binades).
+// one (the tests check every significand).
 struct Kv4Codes {
   uint32_t lo, hi, params;
 };
@@ -371,11 +374,12 @@ __device__ __forceinline__ Kv4Codes kv4_encode16(uint4 x, uint4 y, bool use) {
 //
 // Work of append and read: d / EACH lanes take the d values of a token and
 // head (EACH = 16 in the append, which divides what a vector costs by fewer
-// lanes; 8 in the read, whose lanes then store side by side); a CTA takes 16 tokens (so that the tokens whose V codes
-// share a sector are handled together) of HEADS heads, HEADS_AT_ONCE of them in
-// each thread with their loads under way together: two in the read (126 us for
-// 128K tokens, 141 us with one), one in the append, whose code then fits the
-// instruction cache (32749 tokens, read back included: 98 us with two).
+// lanes; 8 in the read, whose lanes then store side by side); a CTA takes 16
+// tokens (so that the tokens whose V codes share a sector are handled together)
+// of HEADS heads, HEADS_AT_ONCE of them in each thread with their loads under
+// way together: two in the read (126 us for 128K tokens, 141 us with one), one in
+// the append, whose code then fits the instruction cache (32749 tokens, read back
+// included: 98 us with two).
 constexpr int CACHE_THREADS = 256;
 template <int D, int EACH, int HEADS_AT_ONCE>
 struct CacheCta {
@@ -599,23 +603,30 @@ cudaError_t launch_kv4_plan(const Kv4PlanParams& p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, ra_kv4_plan_kernel, p);
 }
 
+namespace {
+
+template <class T>
+cudaError_t append(const Kv4CopyParams& p, int d, cudaStream_t stream) {
+  return d == 128 ? launch_copy<CacheCta<128, 16, 1>>(ra_kv4_append_kernel<128, T>, p, stream)
+                  : launch_copy<CacheCta<64, 16, 1>>(ra_kv4_append_kernel<64, T>, p, stream);
+}
+
+template <class T>
+cudaError_t read(const Kv4CopyParams& p, int d, cudaStream_t stream) {
+  return d == 128 ? launch_copy<CacheCta<128, 8, 2>>(ra_kv4_read_kernel<128, T>, p, stream)
+                  : launch_copy<CacheCta<64, 8, 2>>(ra_kv4_read_kernel<64, T>, p, stream);
+}
+
+}  // namespace
+
 cudaError_t launch_kv4_append(const Kv4CopyParams& p, int d, int dtype, cudaStream_t stream) {
-  if (dtype == RA_BF16)
-    return d == 128 ? launch_copy<CacheCta<128, 16, 1>>(ra_kv4_append_kernel<128, __nv_bfloat16>, p, stream)
-                    : launch_copy<CacheCta<64, 16, 1>>(ra_kv4_append_kernel<64, __nv_bfloat16>, p, stream);
-  return d == 128 ? launch_copy<CacheCta<128, 16, 1>>(ra_kv4_append_kernel<128, __half>, p, stream)
-                  : launch_copy<CacheCta<64, 16, 1>>(ra_kv4_append_kernel<64, __half>, p, stream);
+  return dtype == RA_BF16 ? append<__nv_bfloat16>(p, d, stream) : append<__half>(p, d, stream);
 }
 
 cudaError_t launch_kv4_read(const Kv4CopyParams& p, int d, int dtype, cudaStream_t stream) {
-  if (dtype == RA_BF16)
-    return d == 128 ? launch_copy<CacheCta<128, 8, 2>>(ra_kv4_read_kernel<128, __nv_bfloat16>, p, stream)
-                    : launch_copy<CacheCta<64, 8, 2>>(ra_kv4_read_kernel<64, __nv_bfloat16>, p, stream);
-  if (dtype == RA_FP16)
-    return d == 128 ? launch_copy<CacheCta<128, 8, 2>>(ra_kv4_read_kernel<128, __half>, p, stream)
-                    : launch_copy<CacheCta<64, 8, 2>>(ra_kv4_read_kernel<64, __half>, p, stream);
-  return d == 128 ? launch_copy<CacheCta<128, 8, 2>>(ra_kv4_read_kernel<128, float>, p, stream)
-                  : launch_copy<CacheCta<64, 8, 2>>(ra_kv4_read_kernel<64, float>, p, stream);
+  return dtype == RA_BF16   ? read<__nv_bfloat16>(p, d, stream)
+         : dtype == RA_FP16 ? read<__half>(p, d, stream)
+                            : read<float>(p, d, stream);
 }
 
 cudaError_t read_and_clear_kv4_cache_status(unsigned long long* out) {

@@ -213,7 +213,8 @@ struct Req : Kv4Req {
   int rows, tiles, pairs, room;
 };
 // Tokens that some row of row tile i sees.
-__device__ __forceinline__ int tile_limit(const Kv4AttnParams& p, const Kv4Req& q, int rows, int i) {
+__device__ __forceinline__ int tile_limit(const Kv4AttnParams& p, const Kv4Req& q, int rows,
+                                          int i) {
   const int last = min((i + 1) * UNIT_ROWS, rows) - 1;
   return max(kv4_limit(p, q, last, rows), 0);
 }
@@ -245,8 +246,8 @@ struct Start {
 };
 
 // Every thread of the CTA takes part.
-__device__ __forceinline__ void find_start(const Kv4AttnParams& p, long long* s_scan, Start* s_start,
-                                           int* s_odd) {
+__device__ __forceinline__ void find_start(const Kv4AttnParams& p, long long* s_scan,
+                                           Start* s_start, int* s_odd) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int each = (p.R + THREADS - 1) / THREADS;
   auto cells = [&](const Req& q) { return static_cast<long long>(q.pairs) * p.Hkv * q.room; };
@@ -364,7 +365,8 @@ __device__ void loader_role(const Kv4AttnParams& p, const Bars& br, uint32_t bas
         x.whole = t1 - t0 == nt;
         x.nan_at = 0x7fffffff;
         pieces[k % UQ] = x;
-        asm volatile("st.shared.s32 [%0], %1;" ::"r"(br.units + 4u * (k % UQ)), "r"(k % UQ) : "memory");
+        asm volatile("st.shared.s32 [%0], %1;" ::"r"(br.units + 4u * (k % UQ)), "r"(k % UQ)
+                     : "memory");
         mbar_arrive(br.unit_full(k));
       }
       __syncwarp();
@@ -415,7 +417,8 @@ drain:
 }
 
 // ------------------------------------------------------------------ unpack
-__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                       uint32_t d) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
 }
@@ -485,7 +488,8 @@ __device__ void unpack_role(const Kv4AttnParams& p, const Bars& br, uint32_t bas
               base + C::OFF_PAR + (tile % NPAR) * TILE_KEYS * 8 + (i >> 1) * 16 + (i & 1) * 4;
           asm volatile("st.shared.f32 [%0], %1;" ::"r"(par),
                        "f"(sz.x * (p.scale_log2 * (4194304.f / Q_SCALE))) : "memory");
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(par + 8), "f"(sz.y * p.scale_log2) : "memory");
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(par + 8), "f"(sz.y * p.scale_log2)
+                       : "memory");
           if (i == 0) held[NRAW + tile % NPAR] = have;
           mbar_arrive(br.par_full(tile % NPAR));
         } else {
@@ -999,8 +1003,8 @@ __device__ void softmax_role(const Kv4AttnParams& p, const Bars& br, uint32_t ba
       const int nan_at = *reinterpret_cast<volatile int*>(&pieces[u].nan_at);
       const bool whole = pieces[u].whole;
       const int n_rows = pieces[u].rows, h = pieces[u].h, row0 = pieces[u].row0;
-      float* part = p.partials + (2ll * blockIdx.x + (static_cast<int>(blockIdx.x) == pieces[u].c0)) *
-                                     KV4C_PIECE_FLOATS;
+      const bool starts = static_cast<int>(blockIdx.x) == pieces[u].c0;
+      float* part = p.partials + (2ll * blockIdx.x + starts) * KV4C_PIECE_FLOATS;
       long long at[4];                 // of the row's first element in out
       float inv[4];
 #pragma unroll

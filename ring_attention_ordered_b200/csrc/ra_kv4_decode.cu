@@ -97,8 +97,12 @@ __device__ unsigned long long g_status = 0ull;
 template <int D, int NT>
 struct Smem {
   static constexpr int STAGES = 2;   // of two blocks each
-  // One CTA an SM, of 16 warps if their registers allow it: two of 8 make
-  // twice as many units cross CTAs (one request of 1M tokens: 71 us against 67 us).
+  // One CTA an SM: two of 8 warps make twice as many units cross CTAs (one request of
+  // 1M tokens: 71 us against 67 us).  Of 16 warps, with 128 registers a thread, where
+  // what that spills costs less than half the warps: 16 rows at d = 64, which spill
+  // 508 bytes, 37.9 us against 42.2 us with 8 warps (8 x 8 drafts over 4000 tokens, 64
+  // query and 8 K/V heads), 31.1 against 32.1 us (16 x 1 to 8 drafts over 900 to 16000),
+  // 19.2 against 18.8 us (16 x 4 drafts over 8000).  16 rows at d = 128 need 249 registers.
   static constexpr int WARPS = D * NT <= 128 ? 16 : 8;
   static constexpr int THREADS = WARPS * 32;
   static constexpr int WRING = STAGES * 2 * Kv4<D>::BLOCK_BYTES;
@@ -676,7 +680,8 @@ __global__ void __launch_bounds__((Smem<D, NT>::THREADS), 1)
           if (row < rows)
 #pragma unroll
             for (int w = 0; w < WPL; ++w)
-              kv4_store(p, q.first, h, row, g * (D / 8) + 4 * w, D, values(j, cc, w), -mo[j][cc], l[j][cc]);
+              kv4_store(p, q.first, h, row, g * (D / 8) + 4 * w, D, values(j, cc, w), -mo[j][cc],
+                        l[j][cc]);
         }
       continue;
     }
@@ -697,7 +702,8 @@ __global__ void __launch_bounds__((Smem<D, NT>::THREADS), 1)
         }
       }
     if (lane == 0 && (!head || warp == 0))
-      s_group[head ? 0 : 1 + warp] = {min(ROWS, rows - row0), q.first, h, row0, first / per, last / per};
+      s_group[head ? 0 : 1 + warp] = {min(ROWS, rows - row0), q.first, h, row0, first / per,
+                                      last / per};
   }
 
   // ---- units that cross warps: merged by the CTA, their rows dealt over its
@@ -798,7 +804,10 @@ cudaError_t launch(Kv4AttnParams p, int num_sms, int max_ctas, cudaStream_t stre
   const double units = kv4_decode_units(p.T, p.group, p.R, p.Hkv, p.rows_max);
   const double blocks = 4.0 * p.W * p.page / KV4_BLOCK;
   p.cell_shift = 0;
-  while (units * (blocks / (1ll << p.cell_shift) + UNIT_COST + MIN_CELLS * S::WARPS) >= 2e9) ++p.cell_shift;
+  auto cells = [&] {
+    return units * (blocks / (1ll << p.cell_shift) + UNIT_COST + MIN_CELLS * S::WARPS);
+  };
+  while (cells() >= 2e9) ++p.cell_shift;
   ra_kv4_decode_kernel<D, NT><<<grid, S::THREADS, S::BYTES, stream>>>(p);
   return cudaGetLastError();
 }

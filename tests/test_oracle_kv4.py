@@ -50,6 +50,22 @@ def test_codes_are_the_nearest_levels(d):
     assert (np.abs(v - x) <= s[:, None] * (0.5 + 15 * 2.0 ** -10) + 2.0 ** -25 * 16).all()
 
 
+def test_a_fifteenth_by_a_product_and_one_correction():
+    """q = x F, q + F (x - 15 q) with F = fl(1 / 15), fused (Markstein): the
+    correctly rounded x / 15 for every float32 significand.  The binade does not matter: the
+    steps are exact to powers of two, and where the quotient is below 2^-24, as any
+    of a subnormal's would be, the step is 2^-24 whatever its last place."""
+    F = np.float32(1) / np.float32(15)
+    x = (np.arange(1 << 23, dtype=np.uint32) | np.uint32(0x3F800000)).view(np.float32)
+    q = x * F
+    r = x.astype(np.float64) - 15.0 * q.astype(np.float64)   # 28 bits: exact
+    assert np.array_equal(r.astype(np.float32).astype(np.float64), r)
+    s = q.astype(np.float64) + r * np.float64(F)             # the product has 48 bits: exact
+    # rounded to 64 bits first: no matter unless half way between two of 32 bits
+    assert not ((s.view(np.uint64) & np.uint64((1 << 29) - 1)) == np.uint64(1 << 28)).any()
+    assert np.array_equal(s.astype(np.float32), x / np.float32(15))
+
+
 def test_nan_and_infinities():
     x = np.ones((3, 64))
     x[0, 5] = math.nan
