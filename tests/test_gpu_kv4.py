@@ -772,6 +772,129 @@ def test_a_table_far_wider_than_the_lengths(ra):
     attend(ra, b)
 
 
+# ------------------------------------------------------------------ many rows
+CHUNKS = [
+    # lens, query tokens, Hq, Hkv, d, page
+    ([700, 90], [20, 9], 32, 2, 128, 48),               # groups of 16
+    ([1000], [33], 5, 1, 64, 4096),                     # one page holds it all
+    ([260, 200, 1000], [260, 1, 27], 5, 1, 128, 16),    # a prompt, a token, a chunk
+    ([40000], [64], 4, 1, 128, 128),                    # one unit on many CTAs
+    ([40001, 9], [40, 1], 8, 1, 64, 64),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("shape", range(len(CHUNKS)))
+def test_chunks(ra, shape, dtype):
+    lens, n, Hq, Hkv, d, page = CHUNKS[shape]
+    b = Batch(ra, lens, n, Hq, Hkv, d, page, dtype, 200 + shape)
+    ws = ra.kv4_workspace()
+    first = attend(ra, b, out_dtype=torch.float32, workspace=ws)
+    again = attend(ra, b, out_dtype=torch.float32, workspace=ws)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    attend(ra, b, causal=False, workspace=ws)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale,k_scale", [(0.0, 1.0), (1.0, 6.0), (0.125, 40.0)])
+def test_chunks_flat_and_peaked(ra, scale, k_scale, d):
+    """Scores far beyond what the reference in hand allows, of both signs."""
+    attend(ra, Batch(ra, [600, 130], [90, 70], 4, 2, d, 16, torch.bfloat16, 210, k_scale),
+           scale=scale)
+
+
+def test_chunk_of_large_and_small_queries(ra):
+    """Rows with a scale of their own beside ordinary ones, in the same warp."""
+    b = Batch(ra, [200], [100], 2, 1, 64, 16, torch.bfloat16, 211)
+    want = attend(ra, b)
+    b.q[3] = 0
+    b.q[5] *= 2.0 ** -60
+    b.q[40, 0, 5] = 3e4
+    b.q[41] *= 2.0 ** -11
+    got = attend(ra, b)
+    for t in (0, 1, 2, 4, 6, 39, 42, 99):
+        # a warp with such a row forms its scores in another order: by bf16's step
+        assert (got[0][t].float() - want[0][t].float()).abs().max() <= 2.0 ** -6
+    b.q[50] *= 2.0 ** 40       # its weights sit on one key
+    out, _ = ra.kv4_fwd(b.q.cuda(), b.cache, b.table, b.len_t, cu=b.cu, max_q=100)
+    keys, values = (kv4.kv4_values(*x) for x in b.kv[0])
+    s = b.q[50].double().numpy() @ keys[:151, 0].T.astype(np.float64)
+    ref = values[s.argmax(-1), 0]
+    err = np.abs(out[50].double().cpu().numpy() - ref)
+    assert (err <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * np.abs(ref)).all()
+
+
+@pytest.mark.parametrize("n", [90, 200])
+def test_pages_out_of_range_in_a_chunk(ra, n):
+    """A tile with some of its pages missing and one with none of them."""
+    from ring_attention_ordered_b200 import _lib
+    b = Batch(ra, [700], [n], 4, 2, 64, 16, torch.bfloat16, 212)
+    table = b.table.clone()
+    gone = [3, 5] + list(range(16, 24)) + [43]
+    for i, col in enumerate(gone):
+        table[0, col] = (-1, 10 ** 6, -(1 << 31))[i % 3]
+    out, lse = ra.kv4_fwd(b.q.cuda(), b.cache, table, b.len_t, cu=b.cu, causal=False)
+    with pytest.raises(_lib.RingAttnError) as e:
+        ra.check_status()
+    assert e.value.status == _lib.RA_ERR_INVALID_ARG
+    keep = [c for c in range(700) if c // 16 not in gone]
+    b.kv = [tuple(tuple(x[keep] for x in part) for part in b.kv[0])]
+    b.lens = [len(keep)]
+    b.check(out, lse, False, 0.125)
+
+
+@pytest.mark.parametrize("part", ["k", "v"])
+def test_nan_in_a_unit_on_many_ctas(ra, part):
+    b = Batch(ra, [30000], [64], 4, 1, 128, 64, torch.bfloat16, 213)
+    want = attend(ra, b)
+    at = 30000 - 20                     # seen by the query tokens from 44 on
+    own = b.table[0].tolist()
+    slot = i32([own[at // 64] * 64 + at % 64])
+    old = dict(zip("kv", ra.kv4_read(b.cache, slot)))
+    old[part][0, 0, 3] = math.nan
+    ra.kv4_append(old["k"], old["v"], slot, b.cache)
+    out, lse = ra.kv4_fwd(b.q.cuda(), b.cache, b.table, b.len_t, cu=b.cu)
+    ra.check_status()
+    assert torch.equal(out[:44], want[0][:44]) and torch.equal(lse[:44], want[1][:44])
+    assert bool(torch.isnan(out[44:]).all())
+    if part == "k":
+        assert bool(torch.isnan(lse[44:]).all())
+    else:
+        assert torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("n,max_q", [(100, 0), (100, 1), (100, 64), (3, 1000), (3, 2 ** 31 - 1)])
+def test_max_q_need_not_be_tight(ra, n, max_q):
+    """It chooses the kernel: many rows by the decoding kernel, few by the chunk kernel,
+    alone and in a batch.  Either kernel's roundings are allowed for: those of p * step
+    and of p and v to fp16 (see Batch.check), and of a score, ds: d / 16 instructions
+    and four operations that each cut off 2^-23 of sum |q| (15 step + |zero|) at most."""
+    for lens in ([300], [300, 40, 170]):
+        b = Batch(ra, lens, [n] * len(lens), 4, 2, 64, 16, torch.bfloat16, 214)
+        out, lse = ra.kv4_fwd(b.q.cuda(), b.cache, b.table, b.len_t, cu=b.cu, max_q=max_q,
+                              out_dtype=torch.float32)
+        ra.check_status()
+        for i, L in enumerate(lens):
+            q = b.q[i * n:i * n + n].double().numpy()
+            (kc, ks, kz), (vc, vs, vz) = b.kv[i]
+            v = kv4.kv4_values(vc, vs, vz)
+            ref, rl, w = kv4.kv4_attention(q, kv4.kv4_values(kc, ks, kz), v, n, True, 0.125)
+            none = np.isneginf(rl)
+            got, gl = (x[i * n:i * n + n].double().cpu().numpy() for x in (out, lse))
+            assert np.array_equal(none, np.isneginf(gl)) and (got[none] == 0).all()
+            for h in range(4):
+                most = (15 * ks[:, h // 2].astype(np.float64)
+                        + np.abs(kz[:, h // 2].astype(np.float64))).max()
+                ds = 0.125 * np.abs(q[:, h]).sum(-1) * most * (64 / 16 + 4) * 2.0 ** -23
+                ds = ds + 2.0 ** -20
+                assert (np.abs(gl[:, h] - rl[:, h])[~none[:, h]] <= ds[~none[:, h]]).all()
+                big = 15 * vs[:, h // 2].astype(np.float64)
+                av = np.abs(v[:, h // 2].astype(np.float64))
+                tol = w[:, h] @ ((2.0 ** -10 + 2.0 ** -18) * av + 2.0 ** -11 * big[:, None])
+                tol = tol + 2 * ds[:, None] * (w[:, h] @ av) + L * max(av.max(), big.max()) * 2.0 ** -30
+                assert (np.abs(got[:, h] - ref[:, h]) <= tol + 1e-30).all()
+
+
 @pytest.mark.parametrize("n", [1, 70])
 def test_a_cache_of_no_pages(ra, n):
     """Nothing cached: every row is empty; slots and lengths beyond it are reported."""
