@@ -462,6 +462,14 @@ ra_status ring_attn_kv4_workspace_size(size_t* bytes);
  * parts of a sequence (causal = 0 for the earlier ones) merge with
  * ring_attn_merge, which takes out as RA_FP32 and lse in this layout.
  *
+ * Scores, the weights' sums and lse are fp32.  out, also as RA_FP32, carries
+ * roundings to fp16 for the matrix products: of weight times step for requests
+ * of up to 128 rows (query tokens times g; 2^-11 of w 15 step at most for a token
+ * of weight w, and a term below 2^-33 of the row's largest adds to lse and through
+ * the zeros only), of weight and value beyond (2^-11 of w |v| each, a weight below
+ * 2^-30 of the largest adds to lse only).  They lie below the rounding of a bf16 out,
+ * and are about as large as that of an fp16 one.
+ *
  * Lengths and row starts outside the tensors are cut down to them, tokens of
  * pages outside the cache are left out, and where cu falls no attention is
  * computed; ring_attn_check_status reports each as RA_ERR_INVALID_ARG.
@@ -475,8 +483,9 @@ ra_status ring_attn_kv4_workspace_size(size_t* bytes);
  *   cu       int32 [R + 1] or NULL                                     (in)
  *   out      [T, Hq, d] of q's type, or fp32 (`out_dtype`)            (out)
  *   lse      fp32 [T, Hq], natural log                                (out)
- *   max_q    at least the most query tokens of a request; chooses the kernel,
- *            the result does not need it to be tight
+ *   max_q    at least the most query tokens of a request; it chooses the kernels:
+ *            up to 128 rows one launch, beyond it two (one if R is 1), so the
+ *            number itself is best; the result does not need it to be tight
  *   workspace  ring_attn_kv4_workspace_size bytes                  (in/out)
  *
  * T < 2^31, Hq % Hkv == 0, W >= 1, W * page <= 2^30; tiles of 8 rows (query

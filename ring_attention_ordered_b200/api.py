@@ -551,7 +551,9 @@ def kv4_fwd(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens: tor
     request), its keys the first lens[r] cached tokens; causal: the query
     tokens are the last of these.  Returns (out [T, Hq, d] of q's type or
     ``out_dtype`` float32, lse fp32 [T, Hq]); rows from cu[R] on are not
-    written.  ``max_q`` bounds the query tokens of a request (default T).
+    written.  ``max_q`` bounds the query tokens of a request (default T) and
+    chooses the kernels: 1 while decoding.  ``out`` carries fp16 roundings of
+    the weights (2^-11 at most) even as float32; ``lse`` does not.
     ``workspace`` (``kv4_workspace``) is made for the call if omitted."""
     T, Hq, dq, qs = _check_rows(q, "q")
     P, Hkv, page, d = _cache_shape(cache)
