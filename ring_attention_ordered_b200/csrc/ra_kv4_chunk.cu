@@ -39,7 +39,8 @@
 // CTAs folds the pieces, in their order.
 //
 // What bounds it, measured: two chunks of 1024 tokens over 16K, 32 query and 8
-// K/V heads, d = 128: 550 us, 923 TFLOP/s, 0.57 of cuBLAS's burst rate.  A tile's
+// K/V heads, d = 128: 556 us, 914 TFLOP/s, 0.56 of cuBLAS's burst rate (at 1.95 GHz;
+// 581 us where the power limit holds the clock at 1.88).  A tile's
 // softmax (2480 clocks) and the P V and Q K^T that wait for it (1430) alternate for
 // each of the two row tiles; neither the tensor pipe nor the MUFU is half busy.
 // P V started on the first half of P, with S read half a tile at a time, lost more
@@ -726,7 +727,8 @@ __device__ __forceinline__ bool fold(const Kv4AttnParams& p, const Piece& x, int
                                      int n, bool starts, bool finish, float* tab, RowSync& sync,
                                      const Ctl& cx) {
   constexpr int LPR = D / 4, RPR = 256 / LPR, V = 8;   // rows a round, rows a thread
-  // pieces in flight (d = 128: 549 us with 1, 553 with 2, two chunks of 1024 over 16K;
+  // pieces in flight (d = 128, before K's codes: 549 us with 1, 553 with 2, two chunks
+  // of 1024 over 16K;
   // d = 64: 93 us and 88 us, 8 chunks of 200 over 3K)
   constexpr int E = D == 128 ? 1 : 2;
   const int rows = min(UNIT_ROWS, x.rows - x.row0);
@@ -1080,7 +1082,7 @@ __device__ void softmax_role(const Kv4AttnParams& p, const Bars& br, uint32_t ba
   // last of every FOLD of them folds their pieces, the last to do so folds these.
   // They are counted as they are done, so that it is mostly the second that this
   // CTA is the last for, and folded at the end: amid the tiles the fold's registers
-  // are theirs (two chunks of 1024 tokens over 16K: 573 us, so 549 us).
+  // are theirs (two chunks of 1024 tokens over 16K, before K's codes: 573 us, so 549 us).
   if (n_cut == 0 || !sync(cx)) return;
   extern __shared__ __align__(1024) uint8_t smem_raw[];   // q is no longer needed
   float* tab = reinterpret_cast<float*>(smem_raw + (base + C::OFF_Q - smem_u32(smem_raw)));

@@ -59,8 +59,10 @@
 //
 // What bounds it, measured: with much work the instruction issue of unpacking
 // (271 instructions a block and head, 55% of the issue slots, the ALU pipe 52%
-// busy): 8 requests of 32K tokens, 32 K/V heads, d = 128 take 196 us, 5570 GB/s
-// of cache, 0.85 of the copy rate.  With little work the chain lens, table, block,
+// busy): 8 requests of 32K tokens, 32 K/V heads, d = 128 take 196 us at 1.95 GHz,
+// 5570 GB/s of cache, 0.85 of the copy rate; it follows the clock, and under a load
+// that lasts, where the power limit holds that at 1.71 GHz, it takes 223 us (0.75).
+// With little work the chain lens, table, block,
 // products, merge: 8.8 us for one request of 509 tokens.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
