@@ -910,7 +910,7 @@ ra_status ring_attn_kv4_fwd(const void* q, int64_t q_stride, const void* cache,
   prm.out_f32 = out_dtype == RA_FP32;
   prm.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   char* ws = static_cast<char*>(workspace);
-  prm.partials = reinterpret_cast<float*>(ws + ra::KV4_COUNTER_BYTES + ra::KV4C_COUNTER_BYTES);
+  prm.partials = reinterpret_cast<float*>(ws + RA_KV4_COUNTER_BYTES);
   prm.wait_limit_ns = g_wait_limit_ns.load();
   prm.rows_max = rows_max;
   prm.rows_min = decode ? kKv4DecodeRows : 0;

@@ -7,6 +7,8 @@
 
 #include <cstdint>
 
+#include "ring_attn.h"
+
 namespace ra {
 
 // Parameters of one forward launch.  The tensor maps describe q, k and v as
@@ -235,9 +237,10 @@ constexpr size_t KV4_COUNTER_BYTES = 3 * KV4_MAX_CTAS * 4;
 constexpr size_t KV4C_COUNTER_BYTES = 3 * KV4C_MAX_CTAS * 4;
 constexpr size_t KV4_PARTIAL_BYTES = 2ull * KV4C_MAX_CTAS * KV4C_PIECE_FLOATS * 4;
 static_assert(KV4_PARTIAL_BYTES >= 2ull * KV4_MAX_CTAS * KV4_PIECE_FLOATS * 4, "partials");
-static_assert(KV4_COUNTER_BYTES + KV4C_COUNTER_BYTES <= 16384, "RA_KV4_COUNTER_BYTES");
-static_assert((KV4_COUNTER_BYTES + KV4C_COUNTER_BYTES) % 16 == 0, "partials are 16-byte aligned");
-constexpr size_t KV4_WORKSPACE_BYTES = KV4_COUNTER_BYTES + KV4C_COUNTER_BYTES + KV4_PARTIAL_BYTES;
+// The partials lie behind all that the caller is told to find zero.
+static_assert(KV4_COUNTER_BYTES + KV4C_COUNTER_BYTES <= RA_KV4_COUNTER_BYTES, "counters");
+static_assert(RA_KV4_COUNTER_BYTES % 16 == 0, "partials are 16-byte aligned");
+constexpr size_t KV4_WORKSPACE_BYTES = RA_KV4_COUNTER_BYTES + KV4_PARTIAL_BYTES;
 
 cudaError_t launch_round_bf16(const float* src, __nv_bfloat16* dst, long long n, int num_sms,
                               cudaStream_t stream);

@@ -568,6 +568,19 @@ def test_any_split_gives_the_result(ra, n):
         _lib.ring_attn_set_max_ctas(0)
 
 
+@pytest.mark.parametrize("n", [1, 4, 80])
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_counters_are_left_zero(ra, n, d):
+    """All of the workspace's first KV4_COUNTER_BYTES, by calls whose units cross CTAs,
+    the first CTA among them."""
+    from ring_attention_ordered_b200 import _lib
+    ws = ra.kv4_workspace()
+    for lens in ([9000], [9000, 70, 20000]):
+        b = Batch(ra, lens, [n] * len(lens), 8, 2, d, 64, torch.bfloat16, 72)
+        attend(ra, b, workspace=ws)
+        assert not bool(ws[:_lib.KV4_COUNTER_BYTES].any())
+
+
 @pytest.mark.parametrize("d,dtype", [(64, torch.float16), (128, torch.bfloat16)])
 @pytest.mark.parametrize("ctas", [1, 2, 5])
 def test_many_short_units_a_cta(ra, ctas, d, dtype):
