@@ -368,8 +368,9 @@ __device__ __forceinline__ Kv4Codes kv4_encode16(uint4 x, uint4 y, bool use) {
   return c;
 }
 
-// Bound: the append by instruction issue (71% of the slots; 32749 tokens, 8
-// heads, d = 128: 48 us, 3600 GB/s), the read by memory latency (128K tokens: 126 us,
+// Bound: the append by instruction issue (71% of the slots) and, between, by the loads
+// that each vector waits for at 42% occupancy (32749 tokens, 8 heads, d = 128: 48 us,
+// 3600 GB/s), the read by memory latency (128K tokens: 126 us,
 // 5400 GB/s, 0.82 of the copy rate).
 //
 // Work of append and read: d / EACH lanes take the d values of a token and
